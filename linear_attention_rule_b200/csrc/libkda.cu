@@ -9,6 +9,9 @@
 #include "libkda.h"
 #include "kda_common.cuh"
 #include "kda_decode.cuh"
+#include "kda_decode_pool.cuh"
+#include "kda_kv_append.cuh"
+#include "kda_kv_decode.cuh"
 #include "kda_prefill_simt.cuh"
 #include "kda_prefill_tc.cuh"
 
@@ -57,6 +60,8 @@ const char* kda_status_string(kda_status s) {
         case KDA_ERR_TIMEOUT: return "a bounded device wait expired";
         case KDA_ERR_BAD_SEQLENS: return "cu_seqlens inconsistent with total_tokens";
         case KDA_ERR_BAD_EMIT_POS: return "an emission position is not a chunk boundary of a sequence";
+        case KDA_ERR_BAD_PAGE: return "a cache position outside the block table, or a page outside the cache";
+        case KDA_ERR_BAD_SLOT: return "a state slot outside the pool";
     }
     return "unknown status";
 }
@@ -308,6 +313,186 @@ kda_status kda_decode_ex(const void* q, const void* k, const void* v, const floa
                          const float* beta, float* state_inout, void* out, int32_t N, int32_t H,
                          int32_t dk, int32_t dv, kda_dtype dt, uint32_t in_flags, kda_stream_t stream) {
     return decode_common(q, k, v, g, beta, state_inout, out, N, H, dk, dv, dt, stream, in_flags);
+}
+
+// ------------------------------------------------------------------------------------------
+// The hybrid stack's decode step: the recurrence over a pool of states, the paged cache and
+// the attention over it.
+namespace {
+
+constexpr int32_t kMaxQ = 16;           // new tokens of a sequence that kda_kv_decode takes
+constexpr int32_t kMaxPageSize = 4096;
+
+// A token stride in elements of `elem` bytes: whole 16-byte units, at least the dense size.
+bool valid_stride(int64_t stride, int64_t dense, int64_t elem) {
+    return stride >= dense && stride <= INT64_MAX / 64 && (stride * elem) % 16 == 0;
+}
+
+// What kda_kv_append and kda_kv_decode check alike.
+kda_status check_cache(const kda_kv_cache* c, kda_dtype dt, int32_t num_seqs, int64_t total_tokens,
+                       const int32_t* cu_seqlens, kda::kv::Cache* out) {
+    if (!c || num_seqs < 0 || total_tokens < 0 || c->num_pages < 0 || c->max_pages < 0 || c->Hkv <= 0 ||
+        c->D <= 0 || c->page_size <= 0)
+        return KDA_ERR_INVALID_ARG;
+    if (dt != KDA_F32 && dt != KDA_BF16) return KDA_ERR_INVALID_ARG;
+    if (c->dt != KDA_F32 && c->dt != KDA_BF16 && c->dt != KDA_E4M3) return KDA_ERR_INVALID_ARG;
+    if (total_tokens > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    if ((c->D != 64 && c->D != 128) || (c->page_size & (c->page_size - 1)) != 0 || c->page_size > kMaxPageSize)
+        return KDA_ERR_UNSUPPORTED;
+    if ((dt == KDA_F32) != (c->dt == KDA_F32)) return KDA_ERR_UNSUPPORTED;
+    if (!cu_seqlens && num_seqs != total_tokens) return KDA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) != 0) return KDA_ERR_INVALID_ARG;
+    if (num_seqs == 0 || total_tokens == 0) return KDA_OK;   // nothing is looked at
+    if (!c->seq_lens || (c->max_pages > 0 && !c->block_table) || (c->num_pages > 0 && (!c->k || !c->v)))
+        return KDA_ERR_INVALID_ARG;
+    if (!aligned16(c->k) || !aligned16(c->v)) return KDA_ERR_INVALID_ARG;
+    const uintptr_t words[] = {reinterpret_cast<uintptr_t>(c->seq_lens), reinterpret_cast<uintptr_t>(c->block_table),
+                               reinterpret_cast<uintptr_t>(c->k_scale), reinterpret_cast<uintptr_t>(c->v_scale)};
+    for (uintptr_t p : words)
+        if ((p & 3u) != 0) return KDA_ERR_INVALID_ARG;
+    if ((c->k_scale || c->v_scale) && c->dt != KDA_E4M3) return KDA_ERR_INVALID_ARG;
+    const int64_t elem = c->dt == KDA_F32 ? 4 : c->dt == KDA_BF16 ? 2 : 1;
+    if (!valid_stride(c->page_stride, c->D, elem) || !valid_stride(c->head_stride, c->D, elem) ||
+        !valid_stride(c->row_stride, c->D, elem) || c->table_stride < c->max_pages)
+        return KDA_ERR_INVALID_ARG;
+    int shift = 0;
+    while ((1 << shift) < c->page_size) ++shift;
+    *out = {c->k, c->v, c->k_scale, c->v_scale, c->block_table, c->seq_lens, c->page_stride, c->head_stride,
+            c->row_stride, c->table_stride, c->num_pages, shift, c->max_pages, c->Hkv};
+    return KDA_OK;
+}
+
+// The kernel instance for head size D, the type of q, k, v and the cache's type.
+#define KDA_KV_DISPATCH(launch, D, dt, cdt, ...)                                                        \
+    (dt == KDA_F32 ? (D == 64 ? launch<64, float, float>(__VA_ARGS__) : launch<128, float, float>(__VA_ARGS__)) \
+     : cdt == KDA_BF16                                                                                  \
+         ? (D == 64 ? launch<64, __nv_bfloat16, __nv_bfloat16>(__VA_ARGS__)                             \
+                    : launch<128, __nv_bfloat16, __nv_bfloat16>(__VA_ARGS__))                           \
+         : (D == 64 ? launch<64, __nv_bfloat16, __nv_fp8_e4m3>(__VA_ARGS__)                             \
+                    : launch<128, __nv_bfloat16, __nv_fp8_e4m3>(__VA_ARGS__)))
+
+}  // namespace
+
+kda_status kda_decode_pool(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                           int64_t q_stride, int64_t k_stride, int64_t v_stride, float* state_pool,
+                           int32_t num_slots, const int32_t* slots_in, const int32_t* slots_out,
+                           const int32_t* cu_seqlens, int32_t num_seqs, int64_t total_tokens, int32_t Hk,
+                           int32_t Hv, int32_t dk, int32_t dv, kda_dtype dt, void* out, uint32_t in_flags,
+                           kda_stream_t stream) {
+    if (num_seqs < 0 || total_tokens < 0 || num_slots < 0 || Hk <= 0 || Hv <= 0 || dk <= 0 || dv <= 0)
+        return KDA_ERR_INVALID_ARG;
+    if (in_flags & ~(uint32_t)(KDA_IN_NORMALIZE_QK | KDA_IN_G_LOGITS | KDA_IN_BETA_LOGITS | KDA_IN_G_SCALAR |
+                               KDA_IN_STRONG_DECAY | KDA_IN_SERIAL_CHAINS))
+        return KDA_ERR_INVALID_ARG;
+    if (dt != KDA_F32 && dt != KDA_BF16) return KDA_ERR_INVALID_ARG;
+    if (Hv % Hk != 0 || (!cu_seqlens && num_seqs != total_tokens)) return KDA_ERR_INVALID_ARG;
+    if (!supported_dim(dk, dv) || total_tokens > INT32_MAX || (int64_t)num_seqs * Hv > INT32_MAX)
+        return KDA_ERR_UNSUPPORTED;
+    if ((reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) != 0) return KDA_ERR_INVALID_ARG;
+    if (num_seqs == 0 || total_tokens == 0) return KDA_OK;
+    if (!q || !k || !v || !g || !beta || !slots_in || !slots_out || !out || (num_slots > 0 && !state_pool))
+        return KDA_ERR_INVALID_ARG;
+    const void* ptrs[] = {q, k, v, state_pool, out};
+    for (const void* p : ptrs)
+        if (!aligned16(p)) return KDA_ERR_INVALID_ARG;
+    if (((reinterpret_cast<uintptr_t>(slots_in) | reinterpret_cast<uintptr_t>(slots_out) |
+          reinterpret_cast<uintptr_t>(g) | reinterpret_cast<uintptr_t>(beta)) & 3u) != 0)
+        return KDA_ERR_INVALID_ARG;
+    const int64_t elem = dt == KDA_F32 ? 4 : 2;
+    if (!valid_stride(q_stride, (int64_t)Hk * dk, elem) || !valid_stride(k_stride, (int64_t)Hk * dk, elem) ||
+        !valid_stride(v_stride, (int64_t)Hv * dv, elem))
+        return KDA_ERR_INVALID_ARG;
+    const kda::pool::Params P = {q, k, v, g, beta, q_stride, k_stride, v_stride, state_pool, slots_in, slots_out,
+                                 cu_seqlens, num_slots, num_seqs, Hk, Hv, total_tokens, out, in_flags};
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t err =
+        dt == KDA_F32 ? (dk == 64 ? kda::pool::launch<64, float>(P, st) : kda::pool::launch<128, float>(P, st))
+                      : (dk == 64 ? kda::pool::launch<64, __nv_bfloat16>(P, st)
+                                  : kda::pool::launch<128, __nv_bfloat16>(P, st));
+    return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status kda_kv_append(const void* k, const void* v, const void* q, int64_t k_stride, int64_t v_stride,
+                         int64_t q_stride, kda_dtype dt, const kda_kv_cache* cache, const int32_t* cu_seqlens,
+                         int32_t num_seqs, int64_t total_tokens, int32_t Hq, const kda_rope* rope, void* q_out,
+                         kda_stream_t stream) {
+    kda::append::Params P = {};
+    const kda_status cs = check_cache(cache, dt, num_seqs, total_tokens, cu_seqlens, &P.c);
+    if (cs != KDA_OK) return cs;
+    if (Hq < 0 || (Hq > 0) != (q != nullptr) || (q && !q_out)) return KDA_ERR_INVALID_ARG;
+    if (rope) {
+        if (rope->rot_dim <= 0 || rope->rot_dim > cache->D || rope->rot_dim % 16 != 0 || rope->num_axes < 1 ||
+            rope->num_axes > 4 || (rope->num_axes > 1 && !rope->positions))
+            return KDA_ERR_INVALID_ARG;
+        int64_t pairs = 0;
+        for (int a = 0; a < 4; ++a) {
+            if (a < rope->num_axes && rope->axis_pairs[a] < 0) return KDA_ERR_INVALID_ARG;
+            pairs += a < rope->num_axes ? rope->axis_pairs[a] : 0;
+            if (pairs > rope->rot_dim / 2) return KDA_ERR_INVALID_ARG;
+            P.axis_end[a] = (int32_t)pairs;
+        }
+        if (pairs != rope->rot_dim / 2) return KDA_ERR_INVALID_ARG;
+        P.rot = rope->rot_dim;
+        P.adjacent = rope->adjacent != 0;
+        P.inv_freq = rope->inv_freq;
+        P.positions = rope->positions;
+    }
+    if (num_seqs == 0 || total_tokens == 0) return KDA_OK;
+    if (!k || !v || (rope && !rope->inv_freq)) return KDA_ERR_INVALID_ARG;
+    const void* ptrs[] = {k, v, q, q_out};
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return KDA_ERR_INVALID_ARG;
+    if (((reinterpret_cast<uintptr_t>(P.inv_freq) | reinterpret_cast<uintptr_t>(P.positions)) & 3u) != 0)
+        return KDA_ERR_INVALID_ARG;
+    const int64_t elem = dt == KDA_F32 ? 4 : 2, D = cache->D;
+    if (!valid_stride(k_stride, cache->Hkv * D, elem) || !valid_stride(v_stride, cache->Hkv * D, elem) ||
+        (q && !valid_stride(q_stride, Hq * D, elem)))
+        return KDA_ERR_INVALID_ARG;
+    // units of work of one token are counted in 32 bits
+    if ((int64_t)(Hq + (int64_t)2 * cache->Hkv) * D > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    if (q == q_out && q && q_stride != Hq * D) return KDA_ERR_INVALID_ARG;   // in place only when dense
+    P.k = k; P.v = v; P.q = q;
+    P.k_stride = k_stride; P.v_stride = v_stride; P.q_stride = q_stride;
+    P.cu = cu_seqlens; P.num_seqs = num_seqs; P.Hq = Hq; P.total = total_tokens; P.q_out = q_out;
+    const cudaError_t err = KDA_KV_DISPATCH(kda::append::launch, cache->D, dt, cache->dt, P,
+                                            reinterpret_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+size_t kda_kv_decode_workspace_size(int32_t num_seqs, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_q) {
+    if (num_seqs < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || (D != 64 && D != 128) || max_q < 1 || max_q > kMaxQ)
+        return 0;
+    return 256;
+}
+
+kda_status kda_kv_decode(const void* q, int64_t q_stride, kda_dtype dt, const kda_kv_cache* cache,
+                         const int32_t* cu_seqlens, int32_t num_seqs, int64_t total_tokens, int32_t max_q,
+                         int32_t Hq, float scale, float softcap, int32_t window, const float* alibi_slopes,
+                         const int32_t* kv_start, void* out, float* lse, void* workspace, size_t ws_bytes,
+                         kda_stream_t stream) {
+    kda::attend::Params P = {};
+    const kda_status cs = check_cache(cache, dt, num_seqs, total_tokens, cu_seqlens, &P.c);
+    if (cs != KDA_OK) return cs;
+    if (Hq <= 0 || Hq % cache->Hkv != 0 || max_q < 1 || window < 0 || !(softcap >= 0.f) || !(scale - scale == 0.f) ||
+        !(softcap - softcap == 0.f))
+        return KDA_ERR_INVALID_ARG;
+    if (max_q > kMaxQ || Hq > 65535 || (int64_t)num_seqs * max_q > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || total_tokens == 0) return KDA_OK;
+    if (!q || !out || !aligned16(q) || !aligned16(out)) return KDA_ERR_INVALID_ARG;
+    const uintptr_t words[] = {reinterpret_cast<uintptr_t>(alibi_slopes), reinterpret_cast<uintptr_t>(kv_start),
+                               reinterpret_cast<uintptr_t>(lse)};
+    for (uintptr_t p : words)
+        if ((p & 3u) != 0) return KDA_ERR_INVALID_ARG;
+    if (!valid_stride(q_stride, (int64_t)Hq * cache->D, dt == KDA_F32 ? 4 : 2)) return KDA_ERR_INVALID_ARG;
+    if (ws_bytes < kda_kv_decode_workspace_size(num_seqs, Hq, cache->Hkv, cache->D, max_q) || !workspace ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return KDA_ERR_INVALID_ARG;
+    P.q = q; P.q_stride = q_stride; P.cu = cu_seqlens; P.num_seqs = num_seqs; P.Hq = Hq; P.max_q = max_q;
+    P.window = window; P.total = total_tokens; P.scale = scale; P.softcap = softcap; P.slopes = alibi_slopes;
+    P.kv_start = kv_start; P.out = out; P.lse = lse;
+    const cudaError_t err = KDA_KV_DISPATCH(kda::attend::launch, cache->D, dt, cache->dt, P,
+                                            reinterpret_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 #ifdef KDA_TRACE
