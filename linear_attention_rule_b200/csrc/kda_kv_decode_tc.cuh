@@ -1,0 +1,706 @@
+// The paged attention on tcgen05: bf16 queries over a bf16 or e4m3 cache.
+//
+// A tile is 128 keys.  Both products have the long side as M, so the few query rows (N = 16, 32
+// or 64) waste nothing of the tensor pipe's 128 lanes:
+//   S^T [keys x N]     = K [keys x D] (K-major, as it lies in the cache) * Q [N x D]
+//   O^T [D x N]       += V^T (MN-major, again as it lies in the cache) * P [keys x N]
+// Keys are TMEM lanes, so a softmax thread owns one key: it masks, scales and exponentiates the
+// rows' scores without a shuffle, keeps its own share of every row's sum, and writes its weights
+// as one 16-byte chunk per 8 rows (P MN-major without swizzle, free of bank conflicts).  Only the
+// running maximum is shared, and the tile that raises it by more than 2^8 is rare (kSlack).
+//
+// Warps: 0-3 softmax and epilogue (TMEM lanes 32 w ..), then the loaders, then one that issues the
+// products.  S and O are double-buffered in TMEM, so the product of the next tile runs during the
+// softmax of this one and the next item starts during the epilogue of the last.
+//
+// bf16 (2 D x 2 bytes a key): the loaders copy rows straight to the swizzled operand images.
+// e4m3: tcgen05 has no product of 8-bit with 16-bit operands, and queries or weights in 8 bits
+// would lose what the scores need.  e4m3 is exact in fp16, so the loaders copy raw rows to a ring
+// of their own and turn them into fp16 images (K and V one buffer each).  Weights then are fp16
+// (2^-11), and a query row is scaled by a power of two to a largest element in [1, 2): bf16 has 8
+// bits, fp16 keeps them all down to 2^-14 of the row's largest, and below that 2^-25 of it.
+#pragma once
+
+#include "kda_kv_decode.cuh"
+#include "kda_kv_decode_simt.cuh"
+
+namespace kda {
+namespace attend {
+
+template <int D, typename TC, int N>
+struct Tc {
+    static constexpr bool F8 = sizeof(TC) == 1;
+    static constexpr int TOK = 128, LW = F8 ? 8 : 4, RPW = TOK / LW;   // loader warps, rows of each
+    static constexpr int THREADS = 32 * (4 + LW + 1);
+    static constexpr int ROWB = D * (int)sizeof(TC), CPR = ROWB / 16;  // a cache row
+    static constexpr int OP = TOK * D * 2;                             // an operand image: D / 64 halves of 128-byte rows
+    static constexpr int HALF = TOK * 128, QHALF = N * 128;
+    static constexpr int RAW = TOK * ROWB;
+    static constexpr int QB = N * D * 2, PB = N * TOK * 2;
+    static constexpr int FIXED = F8 ? 2 * OP : 0;                      // the fp16 images
+    static constexpr int STAGE = 2 * RAW;
+    // Slots are reused when the tile before them is known to be done (see the loaders): queries
+    // need one per stage, and one more where the ring is ahead of the operand images.
+    static constexpr int qslots(int stg) { return stg + (F8 ? 1 : 0); }
+    static constexpr int metas(int stg) { return stg + 2; }
+    static constexpr int misc(int stg) {
+        return metas(stg) * 64 + metas(stg) * 16 + qslots(stg) * N * 8 + N * 8 + 4 * N * 4 + N * 4 + 8 * (2 * stg + 20) + 32;
+    }
+    static constexpr int total(int stg) { return FIXED + stg * STAGE + qslots(stg) * QB + PB + misc(stg); }
+    static constexpr int most(int stg) { return stg > 2 && total(stg) > kMaxSmem ? most(stg - 1) : stg; }
+    static constexpr int STG = most(6), QS = qslots(STG), MD = metas(STG);
+    static constexpr int BYTES = total(STG);
+    static_assert(BYTES <= kMaxSmem, "shared memory of a CTA");
+    static_assert((kGroups + 1) * 8 + 32 * 8 <= STG * STAGE, "the table of work lies where the ring comes");
+    // offsets
+    static constexpr int RING = FIXED, Q = RING + STG * STAGE, PM = Q + QS * QB, META = PM + PB, OKM = META + MD * 64,
+                         RINFO = OKM + MD * 16, MROW = RINFO + QS * N * 8, WRED = MROW + N * 8, FROW = WRED + 4 * N * 4,
+                         BAR = FROW + N * 4;
+    static_assert(META % 16 == 0 && OKM % 16 == 0 && RINFO % 16 == 0 && BAR % 8 == 0, "alignment");
+    // barriers
+    static constexpr int NFULL = F8 ? 1 : STG;
+    static constexpr int FULL = BAR, EMPTY = FULL + 8 * NFULL, VFULL = EMPTY + 8 * NFULL, VFREE = VFULL + 8, MFULL = VFREE + 8,
+                         SFULL = MFULL + 8 * MD, SFREE = SFULL + 16, PFULL = SFREE + 16, PVDONE = PFULL + 8, OFREE = PVDONE + 16,
+                         FIN = OFREE + 16, TMEM = FIN + 8, ABORT = TMEM + 4;
+    static_assert(ABORT + 4 <= BYTES, "misc");
+    static constexpr int TCOLS = 4 * N;   // S twice, O twice
+};
+
+__host__ __device__ constexpr uint32_t idesc16(bool bf16, int M, int N, bool a_mn, bool b_mn) {
+    const uint32_t f = bf16 ? 1u : 0u;
+    return (1u << 4) | (f << 7) | (f << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+    return done != 0;
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 ::"r"(taddr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t lo16) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)lo16, __NV_E4M3);
+    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <int D, typename TC, int N>
+struct TcKernel {
+    typedef Tc<D, TC, N> C;
+    typedef Walk<C::TOK, N> W;
+    static constexpr bool F8 = C::F8;
+    static constexpr int TOK = C::TOK;
+
+    const Params& P;
+    uint8_t* sm;
+    uint32_t sb;
+    int T;   // tiles of this stretch
+
+    __device__ __forceinline__ Meta* meta(int t) const { return reinterpret_cast<Meta*>(sm + C::META) + t % C::MD; }
+    __device__ __forceinline__ void fail() const {
+        kda_set_status(KDA_ERR_TIMEOUT);
+        *reinterpret_cast<volatile uint32_t*>(sm + C::ABORT) = 1;
+    }
+    __device__ __forceinline__ bool aborted() const { return *reinterpret_cast<volatile uint32_t*>(sm + C::ABORT) != 0; }
+
+    // ------------------------------------------------------------------ loaders
+    // The item's query rows (zeros behind them), and what a score of each is multiplied with.
+    __device__ __forceinline__ void load_queries(const W& w, int lw, int lane) {
+        constexpr int E = D / 32, B = 4;   // channels of a lane, rows fetched at a time
+        const int slot = w.item % C::QS, rows = w.s.nq * P.group - w.block * N;
+        uint8_t* q = sm + C::Q + slot * C::QB;
+        float2* info = reinterpret_cast<float2*>(sm + C::RINFO) + slot * N;
+        const float ks = F8 && P.c.k_scale ? P.c.k_scale[w.h] : 1.f;
+        const float scale = P.scale * ks * (P.softcap > 0.f ? 2.f * kLog2e / P.softcap : kLog2e);
+        for (int r0 = lw; r0 < N; r0 += B * C::LW) {
+            uint32_t raw[B][E / 2];
+            float slope[B];
+#pragma unroll
+            for (int x = 0; x < B; ++x) {
+                const int r = r0 + x * C::LW;
+                slope[x] = 0.f;
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) raw[x][e] = 0u;
+                if (r < rows && r < N) {
+                    const int ir = w.block * N + r, tok = ir / P.group, g = ir - tok * P.group;
+                    const char* src = reinterpret_cast<const char*>(static_cast<const __nv_bfloat16*>(P.q) +
+                                                                    (w.s.t0 + tok) * P.q_stride + (w.h * P.group + g) * D) + lane * E * 2;
+                    if constexpr (E == 4) {
+                        const uint2 u = *reinterpret_cast<const uint2*>(src);
+                        raw[x][0] = u.x;
+                        raw[x][1] = u.y;
+                    } else {
+                        raw[x][0] = *reinterpret_cast<const uint32_t*>(src);
+                    }
+                    if (P.slopes) slope[x] = P.slopes[w.h * P.group + g] * kLog2e;
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < B; ++x) {
+                const int r = r0 + x * C::LW;
+                if (r >= N) break;
+                float f = scale;
+                if constexpr (F8) {
+                    float top = 0.f;
+#pragma unroll
+                    for (int e = 0; e < E / 2; ++e)
+                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(raw[x][e] << 16)), fabsf(__uint_as_float(raw[x][e] & 0xffff0000u))));
+                    top = warp_max(top);
+                    const int ex = (int)((__float_as_uint(top) >> 23) & 255u);
+                    const int sh = ex == 0 || ex == 255 ? 0 : ex - 127;   // zeros, and infinities, stay as they are
+                    const float down = scalbnf(1.f, -sh);
+                    f = scalbnf(f, sh);
+#pragma unroll
+                    for (int e = 0; e < E / 2; ++e)
+                        raw[x][e] = pack_half2(__uint_as_float(raw[x][e] << 16) * down, __uint_as_float(raw[x][e] & 0xffff0000u) * down);
+                }
+                const int byte = lane * E * 2;
+                uint8_t* dst = q + (byte >> 7) * C::QHALF + sm100::sw128_off(r, (byte & 127) >> 4) + (byte & 15);
+                if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(raw[x][0], raw[x][1]);
+                else *reinterpret_cast<uint32_t*>(dst) = raw[x][0];
+                if (lane == 0) info[r] = make_float2(f, slope[x]);
+            }
+        }
+    }
+
+    // Starts the copies of the tile that the walk stands at, tile t of this stretch.
+    __device__ __forceinline__ void issue(const W& w, const Place& pl, int t, int lw, int lane) {
+        const int row0 = lw * C::RPW;
+        int64_t off;
+        const bool ok = pl.row(P, w, row0 + lane, lane < C::RPW, (int)sizeof(TC), off);
+        const uint32_t m = __ballot_sync(0xffffffffu, ok);
+        if (lane == 0) {
+            if constexpr (F8) reinterpret_cast<uint16_t*>(sm + C::OKM + (t % C::MD) * 16)[lw] = (uint16_t)m;
+            else reinterpret_cast<uint32_t*>(sm + C::OKM + (t % C::MD) * 16)[lw] = m;
+            if (lw == 0) w.fill(meta(t));
+        }
+        if (w.i == 0) load_queries(w, lw, lane);
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(sb + C::MFULL + 8 * (t % C::MD));
+        constexpr int RPI = 32 / C::CPR, ITER = C::RPW / RPI;   // rows of one instruction of the warp
+        const uint32_t dst = sb + C::RING + (t % C::STG) * C::STAGE;
+        const int ch = lane % C::CPR;
+#pragma unroll
+        for (int it = 0; it < ITER; ++it) {
+            const int rl = it * RPI + lane / C::CPR;
+            const int64_t o = __shfl_sync(0xffffffffu, off, rl) + ch * 16;
+            const bool rok = (m >> rl) & 1;
+            uint32_t d;
+            if constexpr (F8) d = dst + ((lw * ITER + it) * 32 + lane) * 16;   // read back by the lane that wrote it
+            else d = dst + (ch >> 3) * C::HALF + sm100::sw128_off(row0 + rl, ch & 7);
+            cp_async16(d, rok ? pl.kb + o : static_cast<const char*>(P.q), rok);
+            cp_async16(d + C::RAW, rok ? pl.vb + o : static_cast<const char*>(P.q), rok);
+        }
+    }
+
+    // e4m3: raw rows of one operand -> its fp16 image
+    __device__ __forceinline__ void convert(uint32_t raw, uint32_t image, int lw, int lane) {
+        constexpr int RPI = 32 / C::CPR, ITER = C::RPW / RPI;
+        const int ch = lane % C::CPR;
+        uint4 u[ITER];
+#pragma unroll
+        for (int it = 0; it < ITER; ++it)
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u[it].x), "=r"(u[it].y), "=r"(u[it].z), "=r"(u[it].w)
+                         : "r"(raw + ((lw * ITER + it) * 32 + lane) * 16) : "memory");
+#pragma unroll
+        for (int it = 0; it < ITER; ++it) {
+            const int row = lw * C::RPW + it * RPI + lane / C::CPR;
+            const uint32_t a[4] = {u[it].x, u[it].y, u[it].z, u[it].w};
+            uint32_t h[8];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                h[2 * x] = e4m3x2_to_half2(a[x] & 0xffffu);
+                h[2 * x + 1] = e4m3x2_to_half2(a[x] >> 16);
+            }
+            // 16 channels are two chunks; lanes of the two halves of a 128-channel row write them in
+            // opposite order, so that eight lanes cover all banks
+            const uint32_t base = image + (ch >> 2) * C::HALF;
+            const bool swap = (ch >> 2) & 1;
+            const uint32_t c0 = 2 * (ch & 3);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const bool second = (x == 1) != swap;
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(base + sm100::sw128_off(row, c0 + (second ? 1 : 0))),
+                             "r"(second ? h[4] : h[0]), "r"(second ? h[5] : h[1]), "r"(second ? h[6] : h[2]), "r"(second ? h[7] : h[3])
+                             : "memory");
+            }
+        }
+    }
+
+    // All of this warp's writes are visible to the tensor core; one arrival per warp.
+    __device__ __forceinline__ void announce(uint32_t bar, int lane) {
+        sm100::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(bar);
+    }
+
+    __device__ __forceinline__ void loader(W& w, int lw, int lane) {
+        Place pl;
+        const int row = lw * C::RPW + lane;
+        const bool has = lane < C::RPW;
+        if (lw == 0 && lane == 0) P.split[blockIdx.x].last = -1;
+        w.s = seq_info<TOK>(P, w.n, N);
+        w.seek();
+        if (lw == 0 && lane == 0) w.tell_join(P.split + blockIdx.x);
+        pl.item(P, w, (int)sizeof(TC));
+        pl.look(P, w, row, has);
+        auto put = [&](int t) {
+            if (t < T) {
+                issue(w, pl, t, lw, lane);
+                if (t + 1 < T) {
+                    w.next();
+                    if (w.i == 0) {
+                        if (lw == 0 && lane == 0) w.tell_join(P.split + blockIdx.x);
+                        pl.item(P, w, (int)sizeof(TC));
+                    }
+                    pl.look(P, w, row, has);
+                }
+            }
+            cp_async_commit();
+        };
+        bool ok = true;
+        if constexpr (F8) {
+            // Tile t is converted while the copies of the STG - 1 behind it are in flight.  The slots
+            // (queries, meta) of tile t + STG - 1 were last used by tile t - 2 or earlier, whose
+            // values were seen to be done before those of tile t - 1 were converted.
+            for (int t = 0; t < C::STG - 1; ++t) put(t);
+            for (int t = 0; t < T; ++t) {
+                put(t + C::STG - 1);
+                cp_async_wait<C::STG - 1>();
+                const uint32_t raw = sb + C::RING + (t % C::STG) * C::STAGE;
+                if (t > 0 && !sm100::mbar_wait(sb + C::EMPTY, (t - 1) & 1)) { ok = false; break; }
+                convert(raw, sb, lw, lane);
+                announce(sb + C::FULL, lane);
+                if (t > 0 && !sm100::mbar_wait(sb + C::VFREE, (t - 1) & 1)) { ok = false; break; }
+                convert(raw + C::RAW, sb + C::OP, lw, lane);
+                announce(sb + C::VFULL, lane);
+                if (aborted()) break;
+            }
+        } else {
+            // Tile t is copied once tile t - STG is done, and announced LAG tiles later, so that the
+            // tile before the one that is waited for can be in work.
+            constexpr int LAG = C::STG > 2 ? C::STG - 2 : 0;
+            for (int t = 0; t < T + LAG; ++t) {
+                if (t >= C::STG && t < T &&
+                    !sm100::mbar_wait(sb + C::EMPTY + 8 * (t % C::STG), (t / C::STG - 1) & 1)) { ok = false; break; }
+                put(t);
+                if (t >= LAG) {
+                    cp_async_wait<LAG>();
+                    announce(sb + C::FULL + 8 * ((t - LAG) % C::STG), lane);
+                }
+                if (aborted()) break;
+            }
+        }
+        cp_async_wait<0>();
+        if (!ok) fail();
+    }
+
+    // ------------------------------------------------------------------ products
+    __device__ __forceinline__ uint32_t k_image(int t) const { return F8 ? sb : sb + C::RING + (t % C::STG) * C::STAGE; }
+    __device__ __forceinline__ uint32_t v_image(int t) const { return F8 ? sb + C::OP : k_image(t) + C::RAW; }
+    __device__ __forceinline__ uint32_t full_bar(int t) const { return sb + C::FULL + (F8 ? 0 : 8 * (t % C::STG)); }
+    static __device__ __forceinline__ uint32_t full_phase(int t) { return F8 ? t & 1 : (t / C::STG) & 1; }
+
+    // Issued by one thread, in whatever order the operands come: scores of tile s, values of tile p.
+    __device__ __forceinline__ void issuer(uint32_t tmem) {
+        using namespace sm100;
+        constexpr uint32_t id_s = idesc16(!F8, 128, N, false, false), id_o = idesc16(!F8, D, N, true, true);
+        int s = 0, p = 0;
+        uint64_t t0 = 0;
+        bool ok = true;
+        for (uint32_t idle = 0; p < T;) {
+            if (s < T && s < p + 2 && mbar_test(full_bar(s), full_phase(s)) &&
+                (s < 2 || mbar_test(sb + C::SFREE + 8 * (s & 1), ((s >> 1) - 1) & 1))) {
+                tc_fence_after();
+                const uint32_t q = sb + C::Q + (meta(s)->item % C::QS) * C::QB, k = k_image(s);
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x)
+                    umma_bf16(tmem + N * (s & 1), smem_desc(k + (x >> 2) * C::HALF + (x & 3) * 32, 16, 1024, kSwizzle128),
+                              smem_desc(q + (x >> 2) * C::QHALF + (x & 3) * 32, 16, 1024, kSwizzle128), id_s, x > 0);
+                umma_commit(sb + C::SFULL + 8 * (s & 1));
+                if constexpr (F8) umma_commit(sb + C::EMPTY);
+                ++s;
+                idle = 0;
+                continue;
+            }
+            if (p < s && mbar_test(sb + C::PFULL, p & 1) && (!F8 || mbar_test(sb + C::VFULL, p & 1))) {
+                const int item = meta(p)->item;
+                const bool first = meta(p)->flags & kFirst;
+                if (!first || item < 2 || mbar_test(sb + C::OFREE + 8 * (item & 1), ((item >> 1) - 1) & 1)) {
+                    tc_fence_after();
+                    const uint32_t v = v_image(p);
+#pragma unroll
+                    for (int x = 0; x < TOK / 16; ++x)
+                        umma_bf16(tmem + 2 * N + N * (item & 1), smem_desc(v + x * 2048, C::HALF, 1024, kSwizzle128),
+                                  smem_desc(sb + C::PM + x * 256, 128, TOK * 16, 0), id_o, x > 0 || !first);
+                    umma_commit(sb + C::PVDONE + 8 * (p & 1));
+                    umma_commit(F8 ? sb + C::VFREE : sb + C::EMPTY + 8 * (p % C::STG));
+                    ++p;
+                    idle = 0;
+                    continue;
+                }
+            }
+            if (idle++ == 0) t0 = globaltimer_ns();
+            if ((idle & 255u) == 0 && (aborted() || globaltimer_ns() - t0 > 2 * kWaitLimitNs)) { ok = false; break; }
+        }
+        if (!ok) fail();
+        // nothing may still run on the tensor pipe when Tensor Memory is released
+        umma_commit(sb + C::FIN);
+        mbar_wait(sb + C::FIN, 0);
+    }
+
+    // ------------------------------------------------------------------ softmax
+    // This thread's channel of O^T: TMEM lanes are channels, with D = 64 the first 16 of each 32.
+    static __device__ __forceinline__ int channel(int w, int lane) { return D == 128 ? 32 * w + lane : lane < 16 ? 16 * w + lane : -1; }
+    __device__ __forceinline__ static bool finite16(uint32_t x) { return F8 ? (x & 0x7c00u) != 0x7c00u : (x & 0x7f80u) != 0x7f80u; }
+
+    // Keys that some tokens see and some do not take part in the product for all (with weight 0
+    // for those that do not see them), which a NaN or infinity among their values would break: such
+    // elements are taken out of the image, and the channel's rows that see them noted in pos / neg.
+    __device__ __forceinline__ void sanitize(const Meta& mt, int t, bool ok, int w, int lane, uint64_t& pos, uint64_t& neg) {
+        uint8_t* v = sm + (v_image(t) - sb);
+        const int key = 32 * w + lane, j = mt.j0 + key;
+        bool bad = false;
+        if (ok && (j > mt.pos0 || j < mt.all_lo)) {
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+                for (int ch = 0; ch < 8; ++ch) {
+                    const uint4 u = *reinterpret_cast<const uint4*>(v + h * C::HALF + sm100::sw128_off(key, ch));
+                    const uint32_t a[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) bad = bad || !finite16(a[x] & 0xffffu) || !finite16(a[x] >> 16);
+                }
+        }
+        if (!bar_any<1>(bad, 128)) return;
+        volatile uint32_t* bits = reinterpret_cast<volatile uint32_t*>(sm + C::WRED);
+        const uint32_t mine = __ballot_sync(0xffffffffu, bad);
+        if (lane == 0) bits[w] = mine;
+        sm100::bar_sync_fixed<1>(128);
+        const int d = channel(w, lane);
+        for (int x = 0; x < 4; ++x)
+            for (uint32_t m = bits[x]; m; m &= m - 1) {
+                const int k = 32 * x + __ffs(m) - 1;
+                if (d < 0) continue;
+                uint16_t* e = reinterpret_cast<uint16_t*>(v + (d >> 6) * C::HALF + sm100::sw128_off(k, (d & 63) >> 3) + 2 * (d & 7));
+                const uint32_t val = *e;
+                if (finite16(val)) continue;
+                *e = 0;
+                const bool nan = F8 ? (val & 0x3ffu) != 0 : (val & 0x7fu) != 0, minus = val & 0x8000u;
+                for (int r = 0; r < mt.rows; ++r) {
+                    const int p = mt.pos0 + (mt.block * N + r) / P.group, jk = mt.j0 + k;
+                    if (jk > p || jk < first_key(P, mt.start, p)) continue;
+                    if (nan || !minus) pos |= 1ull << r;
+                    if (nan || minus) neg |= 1ull << r;
+                }
+            }
+        sm100::bar_sync_fixed<1>(128);   // the list has been read
+    }
+
+    // (out - weighted sum, in fp32) of row r: what sanitize has noted
+    static __device__ __forceinline__ float poisoned(float x, int r, uint64_t pos, uint64_t neg) {
+        if ((pos >> r) & 1) x += INFINITY;
+        if ((neg >> r) & 1) x -= INFINITY;
+        return x;
+    }
+
+    __device__ __forceinline__ void softmax(uint32_t tmem, int w, int lane) {
+        using namespace sm100;
+        constexpr int WD = N < 32 ? N : 32, HB = N / WD;   // rows in registers at a time
+        const int tid = 32 * w + lane, key = tid;
+        const uint32_t tl = tmem + ((uint32_t)(32 * w) << 16);
+        float2* mrow = reinterpret_cast<float2*>(sm + C::MROW);   // (maximum + slack, maximum or 0)
+        float* wred = reinterpret_cast<float*>(sm + C::WRED);
+        float* frow = reinterpret_cast<float*>(sm + C::FROW);
+        const float cap2 = P.softcap * kLog2e;
+        float l[N];
+        uint64_t pos = 0, neg = 0;
+        bool bad = false;
+        for (int t = 0; t < T; ++t) {
+            bad = bad || !mbar_wait(sb + C::MFULL + 8 * (t % C::MD), (t / C::MD) & 1);
+            bad = bad || !mbar_wait(sb + C::SFULL + 8 * (t & 1), (t >> 1) & 1);
+            if (t > 0) bad = bad || !mbar_wait(sb + C::PVDONE + 8 * ((t - 1) & 1), ((t - 1) >> 1) & 1);
+            const Meta mt = *meta(t);
+            const bool first = mt.flags & kFirst, edge = mt.flags & kEdge;
+            if (first) {
+                if (tid < N) mrow[tid] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+                for (int r = 0; r < N; ++r) l[r] = 0.f;
+                pos = neg = 0;
+            }
+            if (bar_any<1>(bad || aborted(), 128)) break;
+            tc_fence_after();
+            const bool ok = (reinterpret_cast<const uint32_t*>(sm + C::OKM + (t % C::MD) * 16)[w] >> lane) & 1;
+            const bool mask = edge || !__all_sync(0xffffffffu, ok);
+            const float2* info = reinterpret_cast<const float2*>(sm + C::RINFO) + (mt.item % C::QS) * N;
+            const uint32_t tS = tl + N * (t & 1), tO = tl + 2 * N + N * (mt.item & 1);
+            const int j = mt.j0 + key;
+#pragma unroll
+            for (int hb = 0; hb < HB; ++hb) {
+                if (32 * hb >= mt.rows) break;
+                float s[WD];
+                if constexpr (WD == 32) tmem_ld32(tS + 32 * hb, s);
+                else tmem_ld16(tS, s);
+                tmem_wait_ld();
+                bool up = false;
+                int tok = (mt.block * N + 32 * hb) / P.group, left = (tok + 1) * P.group - (mt.block * N + 32 * hb);
+#pragma unroll
+                for (int c = 0; c < WD; c += 8) {
+                    if (32 * hb + c >= mt.rows) break;
+                    if (P.softcap > 0.f) {
+                        // cap tanh(x / cap) = cap (1 - 2 / (1 + e^{2 x / cap})): off by up to 2^-21 cap, far below the
+                        // weights' own rounding
+#pragma unroll
+                        for (int i = c; i < c + 8; ++i)
+                            s[i] = cap2 - 2.f * cap2 * rcp(1.f + ex2(s[i] * info[32 * hb + i].x));
+                    } else {
+#pragma unroll
+                        for (int i = c; i < c + 8; ++i) s[i] *= info[32 * hb + i].x;
+                    }
+                    if (P.slopes || mask) {
+#pragma unroll
+                        for (int i = c; i < c + 8; ++i) {
+                            const int p = mt.pos0 + tok;
+                            if (P.slopes) s[i] += info[32 * hb + i].y * (float)(j - p);
+                            if (mask && !(ok && j <= p && j >= first_key(P, mt.start, p))) s[i] = -INFINITY;
+                            if (--left == 0) { ++tok; left = P.group; }
+                        }
+                    }
+#pragma unroll
+                    for (int i = c; i < c + 8; ++i) up = up || s[i] > mrow[32 * hb + i].x;
+                }
+                if (bar_any<2>(up, 128)) {
+                    // some row's maximum rises: the new one, and what the sums so far are worth in it
+                    float mine = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < WD; c += 8) {
+                        if (32 * hb + c >= mt.rows) break;
+#pragma unroll
+                        for (int i = c; i < c + 8; ++i) {
+                            const float x = warp_max(s[i]);
+                            if (lane == i) mine = x;
+                        }
+                    }
+                    if (lane < WD) wred[w * N + 32 * hb + lane] = mine;
+                    bar_sync_fixed<1>(128);
+                    if (tid < WD) {
+                        const int r = 32 * hb + tid;
+                        const float top = fmaxf(fmaxf(wred[r], wred[N + r]), fmaxf(wred[2 * N + r], wred[3 * N + r]));
+                        const float2 old = mrow[r];
+                        float f = 1.f;
+                        if (top > old.x) {
+                            f = old.x == -INFINITY ? 0.f : ex2(old.y - top);
+                            mrow[r] = make_float2(top + kSlack, top);
+                        }
+                        frow[r] = f;
+                    }
+                    bar_sync_fixed<1>(128);
+#pragma unroll
+                    for (int c = 0; c < WD; c += 8) {
+                        if (32 * hb + c >= mt.rows) break;
+                        if (first) continue;   // nothing summed yet
+                        float o[8];
+                        tmem_ld8(tO + 32 * hb + c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float f = frow[32 * hb + c + i];
+                            l[32 * hb + c + i] *= f;
+                            o[i] *= f;
+                        }
+                        tmem_st8(tO + 32 * hb + c, o);
+                    }
+                    tmem_wait_st();
+                }
+#pragma unroll
+                for (int c = 0; c < WD; c += 8) {
+                    if (32 * hb + c >= mt.rows) break;
+                    uint32_t pk[4];
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2) {
+                        const float a = ex2(s[c + i] - mrow[32 * hb + c + i].y), b = ex2(s[c + i + 1] - mrow[32 * hb + c + i + 1].y);
+                        l[32 * hb + c + i] += a;
+                        l[32 * hb + c + i + 1] += b;
+                        pk[i / 2] = F8 ? pack_half2(a, b) : pack_bf16x2(a, b);
+                    }
+                    *reinterpret_cast<uint4*>(sm + C::PM + ((32 * hb + c) / 8) * (TOK * 16) + key * 16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                }
+            }
+            if (edge) {
+                bad = bad || !mbar_wait(F8 ? sb + C::VFULL : full_bar(t), F8 ? t & 1 : full_phase(t));
+                sanitize(mt, t, ok, w, lane, pos, neg);
+            }
+            tc_fence_before();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(sb + C::SFREE + 8 * (t & 1));
+                mbar_arrive(sb + C::PFULL);
+            }
+            if (mt.flags & kLast) {
+                bad = bad || !mbar_wait(sb + C::PVDONE + 8 * (t & 1), (t >> 1) & 1);
+                tc_fence_after();
+                epilogue(mt, tO, l, pos, neg, w, lane);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sb + C::OFREE + 8 * (mt.item & 1));
+            }
+        }
+        if (bad) fail();
+    }
+
+    __device__ __forceinline__ void epilogue(const Meta& mt, uint32_t tO, float (&l)[N], uint64_t pos, uint64_t neg, int w, int lane) {
+        using namespace sm100;
+        const float2* mrow = reinterpret_cast<const float2*>(sm + C::MROW);
+        float* wred = reinterpret_cast<float*>(sm + C::WRED);
+        float* frow = reinterpret_cast<float*>(sm + C::FROW);
+        const int tid = 32 * w + lane, d = channel(w, lane);
+        float* to = P.partial + (int64_t)mt.part * (N * (D + 2));
+        // sums over the warp's keys: lane i of the first 16 ends with row 16 x + i
+#pragma unroll
+        for (int x = 0; x < N / 16; ++x) {
+            if (16 * x >= mt.rows) break;
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = l[16 * x + i] + __shfl_xor_sync(0xffffffffu, l[16 * x + i], 16);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+                for (int i = 0; i < o; ++i) {
+                    const bool hi = lane & o;
+                    const float give = hi ? v[i] : v[i + o], keep = hi ? v[i + o] : v[i];
+                    v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                }
+            if (lane < 16) wred[w * N + 16 * x + lane] = v[0];
+        }
+        bar_sync_fixed<1>(128);
+        if (tid < mt.rows) {
+            const float sum = wred[tid] + wred[N + tid] + wred[2 * N + tid] + wred[3 * N + tid];
+            const float2 m = mrow[tid];
+            if (mt.part < 0) {
+                const int ir = mt.block * N + tid, tok = ir / P.group;
+                const float vs = F8 && P.c.v_scale ? P.c.v_scale[mt.h] : 1.f;
+                frow[tid] = sum == 0.f ? 0.f : vs / sum;
+                if (P.lse)
+                    P.lse[(mt.t0 + tok) * P.Hq + mt.h * P.group + (ir - tok * P.group)] = sum == 0.f ? -INFINITY : m.y * kLn2 + logf(sum);
+            } else {
+                to[tid] = m.x == -INFINITY ? -INFINITY : m.y;
+                to[N + tid] = sum;
+            }
+        }
+        bar_sync_fixed<1>(128);
+        int tok = (mt.block * N) / P.group, left = (tok + 1) * P.group - mt.block * N;
+        int64_t at = (mt.t0 + tok) * P.Hq + mt.h * P.group + (P.group - left);   // output row
+#pragma unroll 1
+        for (int c = 0; c < mt.rows; c += 8) {
+            float o[8];
+            tmem_ld8(tO + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = c + i;
+                if (r < mt.rows && d >= 0) {
+                    const float x = pos | neg ? poisoned(o[i], r, pos, neg) : o[i];
+                    if (mt.part < 0) static_cast<__nv_bfloat16*>(P.out)[at * D + d] = __float2bfloat16_rn(x * frow[r]);
+                    else to[2 * N + r * D + d] = x;
+                }
+                ++at;
+                if (--left == 0) { at += P.Hq - P.group; left = P.group; }
+            }
+        }
+    }
+
+    __device__ __forceinline__ void run() {
+        const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+        W w(P);
+        w.template find<C::THREADS>(reinterpret_cast<int64_t*>(sm + C::RING));
+        kda_grid_launch_next();
+        T = (int)(w.end - w.begin);
+        if (T == 0) {
+            if (tid == 0) P.split[blockIdx.x].last = -1;
+            return;
+        }
+        if (warp == 0) sm100::tmem_alloc(sb + C::TMEM, C::TCOLS);
+        if (tid == 32) {
+            for (int i = 0; i < C::NFULL; ++i) {
+                sm100::mbar_init(sb + C::FULL + 8 * i, C::LW);
+                sm100::mbar_init(sb + C::EMPTY + 8 * i, 1);
+            }
+            sm100::mbar_init(sb + C::VFULL, C::LW);
+            sm100::mbar_init(sb + C::VFREE, 1);
+            for (int i = 0; i < C::MD; ++i) sm100::mbar_init(sb + C::MFULL + 8 * i, C::LW);
+            for (int i = 0; i < 2; ++i) {
+                sm100::mbar_init(sb + C::SFULL + 8 * i, 1);
+                sm100::mbar_init(sb + C::SFREE + 8 * i, 4);
+                sm100::mbar_init(sb + C::PVDONE + 8 * i, 1);
+                sm100::mbar_init(sb + C::OFREE + 8 * i, 4);
+            }
+            sm100::mbar_init(sb + C::PFULL, 4);
+            sm100::mbar_init(sb + C::FIN, 1);
+            sm100::fence_mbar_init();
+            *reinterpret_cast<volatile uint32_t*>(sm + C::ABORT) = 0;
+        }
+        sm100::tc_fence_before();
+        __syncthreads();
+        sm100::tc_fence_after();
+        const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + C::TMEM);
+        if (warp < 4) {
+            softmax(tmem, warp, lane);
+        } else if (warp < 4 + C::LW) {
+            loader(w, warp - 4, lane);
+        } else if (lane == 0) {
+            issuer(tmem);
+        }
+        sm100::tc_fence_before();
+        __syncthreads();
+        sm100::tc_fence_after();
+        if (warp == 0) sm100::tmem_dealloc(tmem, C::TCOLS);
+    }
+};
+
+template <int D, typename TC, int N>
+__global__ void __launch_bounds__(Tc<D, TC, N>::THREADS, 1) attend_tc_kernel(const __grid_constant__ Params P) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    TcKernel<D, TC, N> k{P, smem, sm100::smem_u32(smem), 0};
+    k.run();
+}
+
+template <int D, typename TC, int N>
+cudaError_t launch_tc(const Params& P, cudaStream_t stream) {
+    return launch_pair<D, __nv_bfloat16, TC, N>(attend_tc_kernel<D, TC, N>, Tc<D, TC, N>::THREADS, Tc<D, TC, N>::BYTES, P, stream);
+}
+template <int D, int R>
+cudaError_t launch_simt(const Params& P, cudaStream_t stream) {
+    return launch_pair<D, float, float, R>(attend_simt_kernel<D, R>, Simt<D, R>::THREADS, Simt<D, R>::BYTES, P, stream);
+}
+template <int D, typename T, typename TC>
+cudaError_t launch(const Params& P, cudaStream_t stream) {
+    const int rows = block_rows(sizeof(T) == 4, P.group * P.max_q);
+    if constexpr (sizeof(T) == 4)
+        return rows == 2 ? launch_simt<D, 2>(P, stream) : launch_simt<D, 8>(P, stream);
+    else
+        return rows == 16 ? launch_tc<D, TC, 16>(P, stream) : rows == 32 ? launch_tc<D, TC, 32>(P, stream) : launch_tc<D, TC, 64>(P, stream);
+}
+
+}  // namespace attend
+}  // namespace kda

@@ -11,7 +11,7 @@
 #include "kda_decode.cuh"
 #include "kda_decode_pool.cuh"
 #include "kda_kv_append.cuh"
-#include "kda_kv_decode.cuh"
+#include "kda_kv_decode_tc.cuh"
 #include "kda_prefill_simt.cuh"
 #include "kda_prefill_tc.cuh"
 
@@ -462,7 +462,7 @@ kda_status kda_kv_append(const void* k, const void* v, const void* q, int64_t k_
 size_t kda_kv_decode_workspace_size(int32_t num_seqs, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_q) {
     if (num_seqs < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || (D != 64 && D != 128) || max_q < 1 || max_q > kMaxQ)
         return 0;
-    return kda::attend::workspace_bytes(num_seqs, D, (Hq / Hkv) * max_q);
+    return kda::attend::workspace_bytes(D, (Hq / Hkv) * max_q);
 }
 
 kda_status kda_kv_decode(const void* q, int64_t q_stride, kda_dtype dt, const kda_kv_cache* cache,
@@ -490,8 +490,8 @@ kda_status kda_kv_decode(const void* q, int64_t q_stride, kda_dtype dt, const kd
     P.q = q; P.q_stride = q_stride; P.cu = cu_seqlens; P.num_seqs = num_seqs; P.Hq = Hq; P.max_q = max_q;
     P.window = window; P.total = total_tokens; P.scale = scale; P.softcap = softcap; P.slopes = alibi_slopes;
     P.kv_start = kv_start; P.out = out; P.lse = lse; P.group = Hq / cache->Hkv;
-    P.first = static_cast<int64_t*>(workspace);
-    P.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kda::attend::header_bytes(num_seqs));
+    P.split = static_cast<kda::attend::Split*>(workspace);
+    P.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kda::attend::header_bytes());
     const cudaError_t err = KDA_KV_DISPATCH(kda::attend::launch, cache->D, dt, cache->dt, P,
                                             reinterpret_cast<cudaStream_t>(stream));
     return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
