@@ -9,17 +9,19 @@
 // their group and the sequence's new tokens (G x tokens rows), 4 D flops per row for 2 D
 // elements.  So the work is cut by bytes alone: all (sequence, kv head, row block) items are laid
 // end to end in tiles of keys, and each of 148 CTAs (one per SM) takes one equal stretch of that
-// line, whatever the lengths.  A CTA's loader warps walk the stretch and stream its tiles through
-// a ring of shared-memory stages; the other warps follow.  Items that lie within one stretch are
+// line, whatever the lengths.  Its tiles go through a ring of shared-memory stages.  Items that lie within one stretch are
 // finished there; the others leave a partial triple per stretch, which the join kernel adds up.
 //
-// The rows of a tile are fetched with 16-byte cp.async, not with TMA boxes: a page may hold one
-// row only and end anywhere in a tile, rows that no token sees are not read at all (they are
-// filled with zeros, so that what the cache holds there cannot reach a product), and e4m3 rows
-// have to pass through registers anyway.  It costs about 650 issue slots of the 10,800 in which
-// an SM's share of the memory bandwidth brings a tile.
+// One warp of a CTA walks its stretch and fetches the tiles with TMA: a box is the part of a page
+// in the tile (page_size rows, or the tile), so pages may end anywhere in a tile; boxes without a
+// visible key are not fetched.  The first version fetched rows with 16-byte cp.async from four warps:
+// it kept the load/store pipe so busy (1,750 of the 3,850 cycles of a 64 KB tile) that the
+// softmax's own shared-memory loads queued behind it.
 #pragma once
 
+#include <algorithm>
+
+#include <cuda.h>
 #include <cuda_fp16.h>
 
 #include "kda_kv_cache.cuh"
@@ -48,6 +50,8 @@ struct Params {
     float* lse;
     kv::Cache c;
     Split* split;      // workspace: one per worker, then
+    int32_t box_shift;   // rows of a TMA box: 1 << box_shift
+    CUtensorMap k_map, v_map, q_map;
     float* partial;    // two partial triples per worker: of the item that began before it, and of the one that goes on
 };
 
@@ -117,13 +121,24 @@ __device__ __forceinline__ float warp_max(float x) {
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
-    // a row that is not to be read is filled with zeros
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+// Bounded wait for an mbarrier phase (about a second); false when it ran out.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
+    if (sm100::mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (clock64() - t0 < 2000000000ll)
+        if (sm100::mbar_try_wait(bar, parity)) return true;
+    return false;
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// TMA box loads; all boxes start at a multiple of 16 bytes of the innermost axis.
+__device__ __forceinline__ void tma4(uint32_t dst, const CUtensorMap* map, int x, int row, int head, int page, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"(map), "r"(x), "r"(row), "r"(head), "r"(page), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap* map, int x, int head, int token, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(map), "r"(x), "r"(head), "r"(token), "r"(bar) : "memory");
 }
 // Barrier ID of `count` threads that tells all of them whether `p` holds for any.
 template <int ID> __device__ __forceinline__ bool bar_any(bool p, uint32_t count) {
@@ -137,7 +152,7 @@ template <int ID> __device__ __forceinline__ bool bar_any(bool p, uint32_t count
     return r != 0;
 }
 
-// What the loaders tell the other warps of a tile.
+// What the fetching warp tells the other warps of a tile.
 struct Meta {
     int64_t t0;
     int32_t j0;          // first key
@@ -267,34 +282,101 @@ struct Walk {
     }
 };
 
-// A loader lane's place in the cache for the tile that is issued next.
-struct Place {
-    const char *kb, *vb;
-    const int32_t* table;
-    int page;
+// The fetching warp.  C: the kernel's layout: TOK keys a tile; operands in blocks of BLK channels,
+// each a run of 128-byte rows (e4m3: the whole row), RAW bytes apart for keys and values.
+template <typename C, int ROWS>
+struct Fetch {
+    static constexpr int RPL = C::TOK / 32;   // rows of a lane
+    typedef Walk<C::TOK, ROWS> W;
 
-    template <typename W>
-    __device__ __forceinline__ void item(const Params& P, const W& w, int esz) {
-        const int64_t off = w.h * P.c.head_stride * esz;
-        kb = static_cast<const char*>(P.c.k) + off;
-        vb = static_cast<const char*>(P.c.v) + off;
-        table = P.c.table + w.n * P.c.table_stride;
+    const Params& P;
+    int lane;
+    int page[RPL];   // of the lane's rows in the tile that is fetched next, -1 where none is needed
+
+    // The lane's row x lies in a box with a visible key.
+    __device__ __forceinline__ bool needed(const W& w, int x) const {
+        const int r = (lane * RPL + x) >> P.box_shift << P.box_shift, j = w.j0() + r;
+        return j + (1 << P.box_shift) > w.s.lo && j < w.s.hi && w.s.hi > w.s.lo;
     }
-    template <typename W>
-    __device__ __forceinline__ void look(const Params& P, const W& w, int row, bool has) {
-        const int j = w.j0() + row;
-        page = -1;
-        if (has && j >= w.s.lo && j < w.s.hi) page = __ldg(table + (j >> P.c.page_shift));
+    __device__ __forceinline__ void look(const W& w) {
+        const int32_t* table = P.c.table + w.n * P.c.table_stride;
+#pragma unroll
+        for (int x = 0; x < RPL; ++x) {
+            page[x] = -1;
+            if (needed(w, x)) page[x] = __ldg(table + ((w.j0() + lane * RPL + x) >> P.c.page_shift));
+        }
     }
-    // The lane's row: whether it is read, and its byte offset.
-    template <typename W>
-    __device__ __forceinline__ bool row(const Params& P, const W& w, int row, bool has, int esz, int64_t& off) const {
-        const int j = w.j0() + row;
-        const bool wanted = has && j >= w.s.lo && j < w.s.hi;
-        const bool ok = wanted && page >= 0 && page < P.c.num_pages;
-        if (wanted && !ok) kda_set_status(KDA_ERR_BAD_PAGE);
-        off = ok ? (page * P.c.page_stride + (j & ((1 << P.c.page_shift) - 1)) * P.c.row_stride) * esz : 0;
-        return ok;
+    // Fetches the tile that the walk stands at (and, with an item's first, its queries at q) and
+    // fills in what the others need to know of it.
+    __device__ __forceinline__ void put(const W& w, uint32_t stage, uint32_t q, uint32_t bar, uint32_t meta_bar, Meta* meta, uint32_t* okm) {
+        const int j0 = w.j0(), box = 1 << P.box_shift;
+        uint32_t bits = 0, boxes = 0;
+        bool wrong = false;
+#pragma unroll
+        for (int x = 0; x < RPL; ++x) {
+            const int r = lane * RPL + x, j = j0 + r;
+            const bool need = needed(w, x), ok = need && page[x] >= 0 && page[x] < P.c.num_pages;
+            wrong = wrong || (need && !ok);
+            if (ok && j >= w.s.lo && j < w.s.hi) bits |= 1u << x;
+            if (ok && (r & (box - 1)) == 0) ++boxes;
+            if (!ok) page[x] = -1;
+        }
+        if (wrong) kda_set_status(KDA_ERR_BAD_PAGE);
+        bits <<= (lane * RPL) & 31;
+#pragma unroll
+        for (int o = 1; o < 32 / RPL; o <<= 1) bits |= __shfl_xor_sync(0xffffffffu, bits, o);
+        if (lane % (32 / RPL) == 0) okm[lane * RPL / 32] = bits;
+        boxes = __reduce_add_sync(0xffffffffu, boxes);
+        if (lane == 0) w.fill(meta);
+        __syncwarp();
+        if (lane == 0) {
+            sm100::mbar_arrive(meta_bar);
+            sm100::mbar_arrive_expect_tx(bar, boxes * (uint32_t)(2 * box * C::ROWB) + (w.i == 0 ? C::QB : 0));
+        }
+        __syncwarp();
+        if (w.i == 0) {
+            const int rows = w.s.nq * P.group - w.block * ROWS;
+            for (int r = lane; r < ROWS; r += 32) {
+                const int ir = w.block * ROWS + r, tok = ir / P.group, g = ir - tok * P.group;
+                // rows behind the item's: a token behind the last one, which TMA fills with zeros
+                const int head = r < rows ? w.h * P.group + g : 0, token = r < rows ? (int)w.s.t0 + tok : (int)P.total;
+#pragma unroll
+                for (int b = 0; b < C::QBLKS; ++b)
+                    tma3(q + b * C::QBLOCK + r * C::QROWB, &P.q_map, b * (C::D / C::QBLKS), head, token, bar);
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < RPL; ++x) {
+            const int r = lane * RPL + x;
+            if (page[x] < 0 || (r & (box - 1)) != 0) continue;
+            const int row = (j0 + r) & ((1 << P.c.page_shift) - 1);
+            const uint32_t dst = stage + r * C::pitch(P.box_shift);
+#pragma unroll
+            for (int b = 0; b < C::BLKS; ++b) {
+                tma4(dst + b * C::BLOCK, &P.k_map, b * (C::D / C::BLKS), row, w.h, page[x], bar);
+                tma4(dst + C::RAW + b * C::BLOCK, &P.v_map, b * (C::D / C::BLKS), row, w.h, page[x], bar);
+            }
+        }
+    }
+    // The whole stretch of T tiles.  free(t): waits until stage, queries and meta of tile t may be
+    // overwritten; at(t): where they are.
+    template <typename Free, typename Put>
+    __device__ __forceinline__ bool run(W& w, int T, Free free, Put at) {
+        if (lane == 0) P.split[blockIdx.x].last = -1;
+        w.s = seq_info<C::TOK>(P, w.n, ROWS);
+        w.seek();
+        if (lane == 0) w.tell_join(P.split + blockIdx.x);
+        look(w);
+        for (int t = 0; t < T; ++t) {
+            if (!free(t)) return false;
+            at(t);
+            if (t + 1 < T) {
+                w.next();
+                if (w.i == 0 && lane == 0) w.tell_join(P.split + blockIdx.x);
+                look(w);
+            }
+        }
+        return true;
     }
 };
 
@@ -359,6 +441,50 @@ inline int block_rows(bool f32, int rows) {
 inline size_t header_bytes() { return (sizeof(Split) * kWorkers + 255) & ~(size_t)255; }
 inline size_t workspace_bytes(int D, int rows) {
     return header_bytes() + (size_t)kWorkers * 2 * block_rows(false, rows) * (D + 2) * 4;
+}
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+// cuTensorMapEncodeTiled through the runtime's driver entry point (no link against libcuda).
+inline EncodeFn encode_fn() {
+    static const EncodeFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess && q == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<EncodeFn>(p);
+        return static_cast<EncodeFn>(nullptr);
+    }();
+    return fn;
+}
+
+// The maps of the caches (channels, rows of a page, heads, pages) and of the queries (channels,
+// heads, tokens) for a kernel of layout C.
+template <typename C>
+bool make_maps(Params& P, int64_t D, int esz, CUtensorMapDataType type, CUtensorMapDataType qtype) {
+    const EncodeFn encode = encode_fn();
+    if (!encode) return false;
+    int box = P.c.page_shift;
+    while ((1 << box) > C::TOK) --box;
+    P.box_shift = box;
+    const cuuint64_t one = (cuuint64_t)D * esz;   // a stride that no coordinate uses
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)1 << P.c.page_shift, (cuuint64_t)P.c.Hkv, (cuuint64_t)std::max(P.c.num_pages, 1)};
+    const cuuint64_t strides[3] = {dims[1] > 1 ? (cuuint64_t)P.c.row_stride * esz : one, dims[2] > 1 ? (cuuint64_t)P.c.head_stride * esz : one,
+                                   dims[3] > 1 ? (cuuint64_t)P.c.page_stride * esz : one};
+    const cuuint32_t boxes[4] = {(cuuint32_t)(D / C::BLKS), 1u << box, 1, 1}, ones[4] = {1, 1, 1, 1};
+    const CUtensorMapSwizzle swizzle = C::SWIZZLED ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE;
+    for (int x = 0; x < 2; ++x)
+        // without pages nothing is read
+        if (encode(x ? &P.v_map : &P.k_map, type, 4, P.c.num_pages == 0 ? const_cast<void*>(P.q) : x ? P.c.v : P.c.k, dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return false;
+    const int qsz = qtype == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 4 : 2;
+    const cuuint64_t qdims[3] = {(cuuint64_t)D, (cuuint64_t)P.Hq, (cuuint64_t)P.total};
+    const cuuint64_t qstrides[2] = {(cuuint64_t)D * qsz, (cuuint64_t)(P.total > 1 ? P.q_stride : P.Hq * D) * qsz};
+    const cuuint32_t qbox[3] = {(cuuint32_t)(D / C::QBLKS), 1, 1};
+    return encode(&P.q_map, qtype, 3, const_cast<void*>(P.q), qdims, qstrides, qbox, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  C::QSWIZZLED ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The attention kernel (one CTA per worker), then the join.

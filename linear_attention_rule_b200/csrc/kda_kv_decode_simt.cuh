@@ -12,17 +12,22 @@
 namespace kda {
 namespace attend {
 
-template <int D, int R>
+template <int D_, int R>
 struct Simt {
-    static constexpr int TOK = 32 * 128 / D, LW = 4, RPW = TOK / LW, CW = 8, THREADS = 32 * (LW + CW);
-    static constexpr int ROWB = 4 * D, CPR = ROWB / 16, RAW = TOK * ROWB, STAGE = 2 * RAW;
-    static constexpr int STG = 5, QS = STG, MD = STG + 2;
+    static constexpr int D = D_;
+    static constexpr int TOK = 32 * 128 / D, CW = 8, THREADS = 32 * (CW + 1);
+    static constexpr int ROWB = 4 * D, RAW = TOK * ROWB, STAGE = 2 * RAW;
+    // for Fetch: blocks of 32 channels, 128-byte rows
+    static constexpr bool SWIZZLED = true, QSWIZZLED = false;
+    static constexpr int BLKS = D / 32, BLOCK = TOK * 128, QBLKS = 1, QROWB = ROWB, QBLOCK = 0;
+    static __host__ __device__ constexpr int pitch(int) { return 128; }
+    static constexpr int STG = 6, QS = STG, MD = STG + 2;
     static constexpr int PARTS = 32 * CW / TOK, KPW = 32 / PARTS;    // lanes of a key, keys of a warp
     static constexpr int GROUPS = 32 * CW / D;                       // threads of a channel, 16 keys each
     static constexpr int QB = R * D * 4;
-    static constexpr int Q = STG * STAGE, SC = Q + QS * QB, RED = SC + 2 * R * TOK * 4, META = RED + GROUPS * R * D * 4,
-                         OKM = META + MD * 64, FROW = OKM + MD * 16, ML = FROW + 2 * R * 4, FULL = ML + 2 * R * 4,
-                         EMPTY = FULL + 8 * STG, ABORT = EMPTY + 8 * STG, BYTES = ABORT + 16;
+    static constexpr int Q = STG * STAGE, SC = Q + QS * QB, RED = SC + 2 * R * TOK * 4;
+    static constexpr int META = RED + R * D * 4, OKM = META + MD * 64, FROW = OKM + MD * 16, ML = FROW + 2 * R * 4, FULL = ML + 2 * R * 4,
+                         EMPTY = FULL + 8 * STG, MFULL = EMPTY + 8 * STG, ABORT = MFULL + 8 * MD, BYTES = ABORT + 16;
     static_assert(BYTES <= kMaxSmem && META % 16 == 0 && FULL % 8 == 0, "shared memory of a CTA");
 };
 
@@ -44,73 +49,25 @@ struct SimtKernel {
     }
     __device__ __forceinline__ bool aborted() const { return *reinterpret_cast<volatile uint32_t*>(sm + C::ABORT) != 0; }
 
-    __device__ __forceinline__ void issue(const W& w, const Place& pl, int t, int lw, int lane) {
-        const int row0 = lw * C::RPW;
-        int64_t off;
-        const bool ok = pl.row(P, w, row0 + lane, lane < C::RPW, 4, off);
-        const uint32_t m = __ballot_sync(0xffffffffu, ok);
-        if (lane == 0) {
-            reinterpret_cast<uint16_t*>(sm + C::OKM + (t % C::MD) * 16)[lw] = (uint16_t)m;
-            if (lw == 0) w.fill(meta(t));
-        }
-        if (w.i == 0) {   // the item's query rows, zeros behind them
-            const int rows = w.s.nq * P.group - w.block * R;
-            float4* q = reinterpret_cast<float4*>(sm + C::Q + (w.item % C::QS) * C::QB);
-            for (int x = lw * 32 + lane; x < R * D / 4; x += 32 * C::LW) {
-                const int r = x / (D / 4), ir = w.block * R + r, tok = ir / P.group, g = ir - tok * P.group;
-                q[x] = r < rows ? reinterpret_cast<const float4*>(static_cast<const float*>(P.q) + (w.s.t0 + tok) * P.q_stride +
-                                                                  (w.h * P.group + g) * D)[x % (D / 4)]
-                                : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-        }
-        const uint32_t dst = sb + (t % C::STG) * C::STAGE;
-#pragma unroll
-        for (int it = 0; it < C::RPW * C::CPR / 32; ++it) {
-            const int x = it * 32 + lane, rl = x / C::CPR, ch = x % C::CPR, r = row0 + rl;
-            const int64_t o = __shfl_sync(0xffffffffu, off, rl) + ch * 16;
-            const bool rok = (m >> rl) & 1;
-            const uint32_t d = dst + r * C::ROWB + ((ch ^ (r & 7)) << 4);
-            cp_async16(d, rok ? pl.kb + o : static_cast<const char*>(P.q), rok);
-            cp_async16(d + C::RAW, rok ? pl.vb + o : static_cast<const char*>(P.q), rok);
-        }
+    __device__ __forceinline__ void fetcher(W& w, int lane) {
+        Fetch<C, R> f{P, lane, {}};
+        const bool ok = f.run(
+            w, T,
+            [&](int t) {
+                return !aborted() && (t < C::STG || wait(sb + C::EMPTY + 8 * (t % C::STG), (t / C::STG - 1) & 1));
+            },
+            [&](int t) {
+                f.put(w, sb + (t % C::STG) * C::STAGE, sb + C::Q + (w.item % C::QS) * C::QB, sb + C::FULL + 8 * (t % C::STG),
+                      sb + C::MFULL + 8 * (t % C::MD), meta(t), reinterpret_cast<uint32_t*>(sm + C::OKM + (t % C::MD) * 16));
+            });
+        if (!ok) fail();
+        // copies still in flight at the end of an aborted run
+        if (aborted())
+            for (int t = max(T - C::STG, 0); t < T; ++t) wait(sb + C::FULL + 8 * (t % C::STG), (t / C::STG) & 1);
     }
 
-    __device__ __forceinline__ void loader(W& w, int lw, int lane) {
-        constexpr int LAG = C::STG - 2;   // as for the tensor-core kernel
-        Place pl;
-        const int row = lw * C::RPW + lane;
-        const bool has = lane < C::RPW;
-        if (lw == 0 && lane == 0) P.split[blockIdx.x].last = -1;
-        w.s = seq_info<TOK>(P, w.n, R);
-        w.seek();
-        if (lw == 0 && lane == 0) w.tell_join(P.split + blockIdx.x);
-        pl.item(P, w, 4);
-        pl.look(P, w, row, has);
-        bool ok = true;
-        for (int t = 0; t < T + LAG; ++t) {
-            if (t < T) {
-                if (t >= C::STG && !sm100::mbar_wait(sb + C::EMPTY + 8 * (t % C::STG), (t / C::STG - 1) & 1)) { ok = false; break; }
-                issue(w, pl, t, lw, lane);
-                if (t + 1 < T) {
-                    w.next();
-                    if (w.i == 0) {
-                        if (lw == 0 && lane == 0) w.tell_join(P.split + blockIdx.x);
-                        pl.item(P, w, 4);
-                    }
-                    pl.look(P, w, row, has);
-                }
-            }
-            cp_async_commit();
-            if (t >= LAG) {
-                cp_async_wait<LAG>();
-                __syncwarp();
-                if (lane == 0) sm100::mbar_arrive(sb + C::FULL + 8 * ((t - LAG) % C::STG));
-            }
-            if (aborted()) break;
-        }
-        cp_async_wait<0>();
-        if (!ok) fail();
-    }
+    // byte offset of 16-byte chunk ch of a key's row
+    static __device__ __forceinline__ int chunk(int key, int ch) { return (ch >> 3) * C::BLOCK + (int)sm100::sw128_off(key, ch & 7); }
 
     __device__ __forceinline__ void consumer(int w, int lane) {
         constexpr uint32_t NT = 32 * C::CW;
@@ -122,11 +79,14 @@ struct SimtKernel {
         float acc[R], m = -INFINITY, l = 0.f;   // m, l: of row w
         bool bad = false;
         for (int t = 0; t < T; ++t) {
-            bad = bad || !sm100::mbar_wait(sb + C::FULL + 8 * (t % C::STG), (t / C::STG) & 1);
+            bad = bad || !wait(sb + C::FULL + 8 * (t % C::STG), (t / C::STG) & 1);
             if (bar_any<1>(bad || aborted(), NT)) break;
             const Meta mt = *meta(t);
-            const bool edge = mt.flags & kEdge;
-            const uint16_t* ok16 = reinterpret_cast<const uint16_t*>(sm + C::OKM + (t % C::MD) * 16);
+            const uint32_t* okm = reinterpret_cast<const uint32_t*>(sm + C::OKM + (t % C::MD) * 16);
+            bool all = true;   // all keys there
+#pragma unroll
+            for (int i = 0; i < TOK / 32; ++i) all = all && okm[i] == 0xffffffffu;
+            const bool edge = (mt.flags & kEdge) || !all;
             const uint8_t* k = sm + (t % C::STG) * C::STAGE;
             const uint8_t* v = k + C::RAW;
             const float* q = reinterpret_cast<const float*>(sm + C::Q + (mt.item % C::QS) * C::QB);
@@ -142,9 +102,9 @@ struct SimtKernel {
                 float4 kk[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    kk[i] = *reinterpret_cast<const float4*>(k + key * C::ROWB + (((i * C::PARTS + part) ^ (key & 7)) << 4));
+                    kk[i] = *reinterpret_cast<const float4*>(k + chunk(key, i * C::PARTS + part));
                 const int j = mt.j0 + key;
-                const bool ok = (ok16[key / C::RPW] >> (key % C::RPW)) & 1;
+                const bool ok = (okm[key >> 5] >> (key & 31)) & 1;
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     if (r >= mt.rows) break;
@@ -193,7 +153,7 @@ struct SimtKernel {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int kx = kg * 16 + i;
-                    vv[i] = *reinterpret_cast<const float*>(v + kx * C::ROWB + (((d >> 2) ^ (kx & 7)) << 4) + (d & 3) * 4);
+                    vv[i] = *reinterpret_cast<const float*>(v + chunk(kx, d >> 2) + (d & 3) * 4);
                 }
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
@@ -221,14 +181,17 @@ struct SimtKernel {
                 for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
                 if (w < R && lane == 0) { ml[w] = m; ml[R + w] = l; }
 #pragma unroll
-                for (int r = 0; r < R; ++r) red[(kg * R + r) * D + d] = acc[r];
-                sm100::bar_sync_fixed<1>(NT);
+                for (int g = 0; g < C::GROUPS; ++g) {   // the groups add up their keys in turn
+                    if (kg == g) {
+#pragma unroll
+                        for (int r = 0; r < R; ++r) red[r * D + d] = g == 0 ? acc[r] : red[r * D + d] + acc[r];
+                    }
+                    sm100::bar_sync_fixed<1>(NT);
+                }
                 float* to = P.partial + (int64_t)mt.part * (R * (D + 2));
                 for (int x = tid; x < mt.rows * D; x += NT) {
                     const int r = x / D, c = x % D;
-                    float a = red[r * D + c];
-#pragma unroll
-                    for (int g = 1; g < C::GROUPS; ++g) a += red[(g * R + r) * D + c];
+                    const float a = red[r * D + c];
                     const float sum = ml[R + r];
                     if (mt.part < 0) {
                         const int ir = mt.block * R + r, tok = ir / P.group;
@@ -257,15 +220,16 @@ struct SimtKernel {
         }
         if (tid == 0) {
             for (int i = 0; i < C::STG; ++i) {
-                sm100::mbar_init(sb + C::FULL + 8 * i, C::LW);
+                sm100::mbar_init(sb + C::FULL + 8 * i, 1);
                 sm100::mbar_init(sb + C::EMPTY + 8 * i, C::CW);
             }
+            for (int i = 0; i < C::MD; ++i) sm100::mbar_init(sb + C::MFULL + 8 * i, 1);
             sm100::fence_mbar_init();
             *reinterpret_cast<volatile uint32_t*>(sm + C::ABORT) = 0;
         }
         __syncthreads();
         if (warp < C::CW) consumer(warp, lane);
-        else loader(w, warp - C::CW, lane);
+        else fetcher(w, lane);
     }
 };
 

@@ -9,16 +9,16 @@
 // as one 16-byte chunk per 8 rows (P MN-major without swizzle, free of bank conflicts).  Only the
 // running maximum is shared, and the tile that raises it by more than 2^8 is rare (kSlack).
 //
-// Warps: 0-3 softmax and epilogue (TMEM lanes 32 w ..), then the loaders, then one that issues the
-// products.  S and O are double-buffered in TMEM, so the product of the next tile runs during the
-// softmax of this one and the next item starts during the epilogue of the last.
+// Warps: 0-3 softmax and epilogue (TMEM lanes 32 w ..), 4 fetches tiles, 5 issues the products, with
+// an e4m3 cache 6-13 convert.  S and O are double-buffered in TMEM, so the product of the next tile
+// runs during the softmax of this one and the next item starts during the epilogue of the last.
 //
-// bf16 (2 D x 2 bytes a key): the loaders copy rows straight to the swizzled operand images.
+// bf16: tiles land in the operand images directly (TMA's 128-byte swizzle is the images').
 // e4m3: tcgen05 has no product of 8-bit with 16-bit operands, and queries or weights in 8 bits
-// would lose what the scores need.  e4m3 is exact in fp16, so the loaders copy raw rows to a ring
-// of their own and turn them into fp16 images (K and V one buffer each).  Weights then are fp16
-// (2^-11), and a query row is scaled by a power of two to a largest element in [1, 2): bf16 has 8
-// bits, fp16 keeps them all down to 2^-14 of the row's largest, and below that 2^-25 of it.
+// would lose what the scores need.  e4m3 is exact in fp16, so raw rows land in a ring of their own
+// and are turned into fp16 images (K and V one buffer each).  Weights then are fp16 (2^-11), and
+// a query row is scaled by a power of two to a largest element in [1, 2): bf16 has 8 bits, fp16
+// keeps them all down to 2^-14 of the row's largest, and below that 2^-25 of it.
 #pragma once
 
 #include "kda_kv_decode.cuh"
@@ -27,24 +27,32 @@
 namespace kda {
 namespace attend {
 
-template <int D, typename TC, int N>
+template <int D_, typename TC, int N>
 struct Tc {
+    static constexpr int D = D_;
     static constexpr bool F8 = sizeof(TC) == 1;
-    static constexpr int TOK = 128, LW = F8 ? 8 : 4, RPW = TOK / LW;   // loader warps, rows of each
-    static constexpr int THREADS = 32 * (4 + LW + 1);
+    static constexpr int TOK = 128, LW = F8 ? 8 : 0, RPW = F8 ? TOK / LW : TOK;   // converting warps, rows of each
+    static constexpr int THREADS = 32 * (6 + LW);
     static constexpr int ROWB = D * (int)sizeof(TC), CPR = ROWB / 16;  // a cache row
     static constexpr int OP = TOK * D * 2;                             // an operand image: D / 64 halves of 128-byte rows
     static constexpr int HALF = TOK * 128, QHALF = N * 128;
-    static constexpr int RAW = TOK * ROWB;
+    static constexpr int RAW = TOK * 128 * (F8 || D == 64 ? 1 : 2);
+    // for Fetch
+    static constexpr bool SWIZZLED = !F8, QSWIZZLED = true;
+    static constexpr int BLKS = F8 ? 1 : D / 64, BLOCK = HALF;
+    // from row to row; a box starts at a multiple of 128 bytes, boxes of one 64-byte row too
+    static __host__ __device__ constexpr int pitch(int box_shift) { return F8 && box_shift > 0 ? ROWB : 128; }
+    static constexpr int QBLKS = D / 64, QROWB = 128, QBLOCK = QHALF;
     static constexpr int QB = N * D * 2, PB = N * TOK * 2;
     static constexpr int FIXED = F8 ? 2 * OP : 0;                      // the fp16 images
     static constexpr int STAGE = 2 * RAW;
-    // Slots are reused when the tile before them is known to be done (see the loaders): queries
-    // need one per stage, and one more where the ring is ahead of the operand images.
+    // Slots are reused once a tile before them is known to be done.  A stage is free when its tile t
+    // is done (bf16), or converted, and then tile t - 1 is done (e4m3): queries need one slot per
+    // stage, e4m3 one more; meta is read a little longer.
     static constexpr int qslots(int stg) { return stg + (F8 ? 1 : 0); }
     static constexpr int metas(int stg) { return stg + 2; }
     static constexpr int misc(int stg) {
-        return metas(stg) * 64 + metas(stg) * 16 + qslots(stg) * N * 8 + N * 8 + 4 * N * 4 + N * 4 + 8 * (2 * stg + 20) + 32;
+        return metas(stg) * 64 + metas(stg) * 16 + qslots(stg) * N * 4 + N * 8 + N * 8 + 4 * N * 4 + N * 4 + 8 * (2 * stg + metas(stg) + 18) + 16;
     }
     static constexpr int total(int stg) { return FIXED + stg * STAGE + qslots(stg) * QB + PB + misc(stg); }
     static constexpr int most(int stg) { return stg > 2 && total(stg) > kMaxSmem ? most(stg - 1) : stg; }
@@ -54,14 +62,13 @@ struct Tc {
     static_assert((kGroups + 1) * 8 + 32 * 8 <= STG * STAGE, "the table of work lies where the ring comes");
     // offsets
     static constexpr int RING = FIXED, Q = RING + STG * STAGE, PM = Q + QS * QB, META = PM + PB, OKM = META + MD * 64,
-                         RINFO = OKM + MD * 16, MROW = RINFO + QS * N * 8, WRED = MROW + N * 8, FROW = WRED + 4 * N * 4,
-                         BAR = FROW + N * 4;
+                         QF = OKM + MD * 16, RINFO = QF + QS * N * 4, MROW = RINFO + N * 8, WRED = MROW + N * 8,
+                         FROW = WRED + 4 * N * 4, BAR = FROW + N * 4;
     static_assert(META % 16 == 0 && OKM % 16 == 0 && RINFO % 16 == 0 && BAR % 8 == 0, "alignment");
     // barriers
-    static constexpr int NFULL = F8 ? 1 : STG;
-    static constexpr int FULL = BAR, EMPTY = FULL + 8 * NFULL, VFULL = EMPTY + 8 * NFULL, VFREE = VFULL + 8, MFULL = VFREE + 8,
-                         SFULL = MFULL + 8 * MD, SFREE = SFULL + 16, PFULL = SFREE + 16, PVDONE = PFULL + 8, OFREE = PVDONE + 16,
-                         FIN = OFREE + 16, TMEM = FIN + 8, ABORT = TMEM + 4;
+    static constexpr int FULL = BAR, EMPTY = FULL + 8 * STG, MFULL = EMPTY + 8 * STG, KFULL = MFULL + 8 * MD, KFREE = KFULL + 8,
+                         VFULL = KFREE + 8, VFREE = VFULL + 8, QFULL = VFREE + 8, SFULL = QFULL + 16, SFREE = SFULL + 16,
+                         PFULL = SFREE + 16, PVDONE = PFULL + 8, OFREE = PVDONE + 16, FIN = OFREE + 16, TMEM = FIN + 8, ABORT = TMEM + 4;
     static_assert(ABORT + 4 <= BYTES, "misc");
     static constexpr int TCOLS = 4 * N;   // S twice, O twice
 };
@@ -123,109 +130,77 @@ struct TcKernel {
     }
     __device__ __forceinline__ bool aborted() const { return *reinterpret_cast<volatile uint32_t*>(sm + C::ABORT) != 0; }
 
-    // ------------------------------------------------------------------ loaders
-    // The item's query rows (zeros behind them), and what a score of each is multiplied with.
-    __device__ __forceinline__ void load_queries(const W& w, int lw, int lane) {
-        constexpr int E = D / 32, B = 4;   // channels of a lane, rows fetched at a time
-        const int slot = w.item % C::QS, rows = w.s.nq * P.group - w.block * N;
-        uint8_t* q = sm + C::Q + slot * C::QB;
-        float2* info = reinterpret_cast<float2*>(sm + C::RINFO) + slot * N;
-        const float ks = F8 && P.c.k_scale ? P.c.k_scale[w.h] : 1.f;
-        const float scale = P.scale * ks * (P.softcap > 0.f ? 2.f * kLog2e / P.softcap : kLog2e);
-        for (int r0 = lw; r0 < N; r0 += B * C::LW) {
-            uint32_t raw[B][E / 2];
-            float slope[B];
-#pragma unroll
-            for (int x = 0; x < B; ++x) {
-                const int r = r0 + x * C::LW;
-                slope[x] = 0.f;
-#pragma unroll
-                for (int e = 0; e < E / 2; ++e) raw[x][e] = 0u;
-                if (r < rows && r < N) {
-                    const int ir = w.block * N + r, tok = ir / P.group, g = ir - tok * P.group;
-                    const char* src = reinterpret_cast<const char*>(static_cast<const __nv_bfloat16*>(P.q) +
-                                                                    (w.s.t0 + tok) * P.q_stride + (w.h * P.group + g) * D) + lane * E * 2;
-                    if constexpr (E == 4) {
-                        const uint2 u = *reinterpret_cast<const uint2*>(src);
-                        raw[x][0] = u.x;
-                        raw[x][1] = u.y;
-                    } else {
-                        raw[x][0] = *reinterpret_cast<const uint32_t*>(src);
-                    }
-                    if (P.slopes) slope[x] = P.slopes[w.h * P.group + g] * kLog2e;
-                }
-            }
-#pragma unroll
-            for (int x = 0; x < B; ++x) {
-                const int r = r0 + x * C::LW;
-                if (r >= N) break;
-                float f = scale;
-                if constexpr (F8) {
-                    float top = 0.f;
-#pragma unroll
-                    for (int e = 0; e < E / 2; ++e)
-                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(raw[x][e] << 16)), fabsf(__uint_as_float(raw[x][e] & 0xffff0000u))));
-                    top = warp_max(top);
-                    const int ex = (int)((__float_as_uint(top) >> 23) & 255u);
-                    const int sh = ex == 0 || ex == 255 ? 0 : ex - 127;   // zeros, and infinities, stay as they are
-                    const float down = scalbnf(1.f, -sh);
-                    f = scalbnf(f, sh);
-#pragma unroll
-                    for (int e = 0; e < E / 2; ++e)
-                        raw[x][e] = pack_half2(__uint_as_float(raw[x][e] << 16) * down, __uint_as_float(raw[x][e] & 0xffff0000u) * down);
-                }
-                const int byte = lane * E * 2;
-                uint8_t* dst = q + (byte >> 7) * C::QHALF + sm100::sw128_off(r, (byte & 127) >> 4) + (byte & 15);
-                if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(raw[x][0], raw[x][1]);
-                else *reinterpret_cast<uint32_t*>(dst) = raw[x][0];
-                if (lane == 0) info[r] = make_float2(f, slope[x]);
-            }
-        }
+    // ------------------------------------------------------------------ fetching
+    __device__ __forceinline__ void fetcher(W& w, int lane) {
+        Fetch<C, N> f{P, lane, {}};
+        const bool ok = f.run(
+            w, T,
+            [&](int t) {
+                return !aborted() && (t < C::STG || wait(sb + C::EMPTY + 8 * (t % C::STG), (t / C::STG - 1) & 1));
+            },
+            [&](int t) {
+                f.put(w, sb + C::RING + (t % C::STG) * C::STAGE, sb + C::Q + (w.item % C::QS) * C::QB, sb + C::FULL + 8 * (t % C::STG),
+                      sb + C::MFULL + 8 * (t % C::MD), meta(t), reinterpret_cast<uint32_t*>(sm + C::OKM + (t % C::MD) * 16));
+            });
+        if (!ok) fail();
+    }
+    // Copies in flight at the end of an aborted run are waited for (a fetch of a whole tile each).
+    __device__ __forceinline__ void drain() {
+        for (int t = max(T - C::STG, 0); t < T; ++t) wait(sb + C::FULL + 8 * (t % C::STG), (t / C::STG) & 1);
     }
 
-    // Starts the copies of the tile that the walk stands at, tile t of this stretch.
-    __device__ __forceinline__ void issue(const W& w, const Place& pl, int t, int lw, int lane) {
-        const int row0 = lw * C::RPW;
-        int64_t off;
-        const bool ok = pl.row(P, w, row0 + lane, lane < C::RPW, (int)sizeof(TC), off);
-        const uint32_t m = __ballot_sync(0xffffffffu, ok);
-        if (lane == 0) {
-            if constexpr (F8) reinterpret_cast<uint16_t*>(sm + C::OKM + (t % C::MD) * 16)[lw] = (uint16_t)m;
-            else reinterpret_cast<uint32_t*>(sm + C::OKM + (t % C::MD) * 16)[lw] = m;
-            if (lw == 0) w.fill(meta(t));
-        }
-        if (w.i == 0) load_queries(w, lw, lane);
+    // ------------------------------------------------------------------ e4m3 -> fp16
+    // All of this warp's writes are visible to the tensor core; one arrival per warp.
+    __device__ __forceinline__ void announce(uint32_t bar, int lane) {
+        sm100::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) sm100::mbar_arrive(sb + C::MFULL + 8 * (t % C::MD));
-        constexpr int RPI = 32 / C::CPR, ITER = C::RPW / RPI;   // rows of one instruction of the warp
-        const uint32_t dst = sb + C::RING + (t % C::STG) * C::STAGE;
-        const int ch = lane % C::CPR;
+        if (lane == 0) sm100::mbar_arrive(bar);
+    }
+    // The item's bf16 query rows, in place; the factor that undoes their scaling in qf.
+    __device__ __forceinline__ void convert_queries(int slot, int lw, int lane) {
+        constexpr int E = D / 32;   // channels of a lane
+        const int byte = lane * E * 2;
+#pragma unroll 2
+        for (int r = lw; r < N; r += C::LW) {
+            uint8_t* at = sm + C::Q + slot * C::QB + (byte >> 7) * C::QHALF + sm100::sw128_off(r, (byte & 127) >> 4) + (byte & 15);
+            uint32_t raw[E / 2];
+            if constexpr (E == 4) {
+                const uint2 u = *reinterpret_cast<const uint2*>(at);
+                raw[0] = u.x;
+                raw[1] = u.y;
+            } else {
+                raw[0] = *reinterpret_cast<const uint32_t*>(at);
+            }
+            float top = 0.f;
 #pragma unroll
-        for (int it = 0; it < ITER; ++it) {
-            const int rl = it * RPI + lane / C::CPR;
-            const int64_t o = __shfl_sync(0xffffffffu, off, rl) + ch * 16;
-            const bool rok = (m >> rl) & 1;
-            uint32_t d;
-            if constexpr (F8) d = dst + ((lw * ITER + it) * 32 + lane) * 16;   // read back by the lane that wrote it
-            else d = dst + (ch >> 3) * C::HALF + sm100::sw128_off(row0 + rl, ch & 7);
-            cp_async16(d, rok ? pl.kb + o : static_cast<const char*>(P.q), rok);
-            cp_async16(d + C::RAW, rok ? pl.vb + o : static_cast<const char*>(P.q), rok);
+            for (int e = 0; e < E / 2; ++e)
+                top = fmaxf(top, fmaxf(fabsf(__uint_as_float(raw[e] << 16)), fabsf(__uint_as_float(raw[e] & 0xffff0000u))));
+            top = warp_max(top);
+            const int ex = (int)((__float_as_uint(top) >> 23) & 255u);
+            const int sh = ex == 0 || ex == 255 ? 0 : ex - 127;   // zeros, and infinities, stay as they are
+            const float down = scalbnf(1.f, -sh);
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e)
+                raw[e] = pack_half2(__uint_as_float(raw[e] << 16) * down, __uint_as_float(raw[e] & 0xffff0000u) * down);
+            if constexpr (E == 4) *reinterpret_cast<uint2*>(at) = make_uint2(raw[0], raw[1]);
+            else *reinterpret_cast<uint32_t*>(at) = raw[0];
+            if (lane == 0) reinterpret_cast<float*>(sm + C::QF)[slot * N + r] = scalbnf(1.f, sh);
         }
     }
-
-    // e4m3: raw rows of one operand -> its fp16 image
-    __device__ __forceinline__ void convert(uint32_t raw, uint32_t image, int lw, int lane) {
+    // raw rows of one operand -> its fp16 image; zeros for rows that no token sees
+    __device__ __forceinline__ void convert(uint32_t raw, uint32_t image, uint32_t ok, int lw, int lane) {
         constexpr int RPI = 32 / C::CPR, ITER = C::RPW / RPI;
-        const int ch = lane % C::CPR;
+        const int ch = lane % C::CPR, pitch = C::pitch(P.box_shift);
         uint4 u[ITER];
 #pragma unroll
         for (int it = 0; it < ITER; ++it)
             asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u[it].x), "=r"(u[it].y), "=r"(u[it].z), "=r"(u[it].w)
-                         : "r"(raw + ((lw * ITER + it) * 32 + lane) * 16) : "memory");
+                         : "r"(raw + (lw * C::RPW + it * RPI + lane / C::CPR) * pitch + ch * 16) : "memory");
 #pragma unroll
         for (int it = 0; it < ITER; ++it) {
-            const int row = lw * C::RPW + it * RPI + lane / C::CPR;
-            const uint32_t a[4] = {u[it].x, u[it].y, u[it].z, u[it].w};
+            const int rl = it * RPI + lane / C::CPR, row = lw * C::RPW + rl;
+            const uint32_t keep = (ok >> rl) & 1 ? 0xffffffffu : 0u;
+            const uint32_t a[4] = {u[it].x & keep, u[it].y & keep, u[it].z & keep, u[it].w & keep};
             uint32_t h[8];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
@@ -246,79 +221,34 @@ struct TcKernel {
             }
         }
     }
-
-    // All of this warp's writes are visible to the tensor core; one arrival per warp.
-    __device__ __forceinline__ void announce(uint32_t bar, int lane) {
-        sm100::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) sm100::mbar_arrive(bar);
-    }
-
-    __device__ __forceinline__ void loader(W& w, int lw, int lane) {
-        Place pl;
-        const int row = lw * C::RPW + lane;
-        const bool has = lane < C::RPW;
-        if (lw == 0 && lane == 0) P.split[blockIdx.x].last = -1;
-        w.s = seq_info<TOK>(P, w.n, N);
-        w.seek();
-        if (lw == 0 && lane == 0) w.tell_join(P.split + blockIdx.x);
-        pl.item(P, w, (int)sizeof(TC));
-        pl.look(P, w, row, has);
-        auto put = [&](int t) {
-            if (t < T) {
-                issue(w, pl, t, lw, lane);
-                if (t + 1 < T) {
-                    w.next();
-                    if (w.i == 0) {
-                        if (lw == 0 && lane == 0) w.tell_join(P.split + blockIdx.x);
-                        pl.item(P, w, (int)sizeof(TC));
-                    }
-                    pl.look(P, w, row, has);
-                }
-            }
-            cp_async_commit();
-        };
+    __device__ __forceinline__ void converter(int lw, int lane) {
         bool ok = true;
-        if constexpr (F8) {
-            // Tile t is converted while the copies of the STG - 1 behind it are in flight.  The slots
-            // (queries, meta) of tile t + STG - 1 were last used by tile t - 2 or earlier, whose
-            // values were seen to be done before those of tile t - 1 were converted.
-            for (int t = 0; t < C::STG - 1; ++t) put(t);
-            for (int t = 0; t < T; ++t) {
-                put(t + C::STG - 1);
-                cp_async_wait<C::STG - 1>();
-                const uint32_t raw = sb + C::RING + (t % C::STG) * C::STAGE;
-                if (t > 0 && !sm100::mbar_wait(sb + C::EMPTY, (t - 1) & 1)) { ok = false; break; }
-                convert(raw, sb, lw, lane);
-                announce(sb + C::FULL, lane);
-                if (t > 0 && !sm100::mbar_wait(sb + C::VFREE, (t - 1) & 1)) { ok = false; break; }
-                convert(raw + C::RAW, sb + C::OP, lw, lane);
-                announce(sb + C::VFULL, lane);
-                if (aborted()) break;
+        for (int t = 0; t < T; ++t) {
+            ok = !aborted() && wait(sb + C::FULL + 8 * (t % C::STG), (t / C::STG) & 1);
+            if (!ok) break;
+            const uint32_t raw = sb + C::RING + (t % C::STG) * C::STAGE;
+            const uint32_t seen = reinterpret_cast<const uint16_t*>(sm + C::OKM + (t % C::MD) * 16)[lw];
+            const int item = meta(t)->item;
+            if (meta(t)->flags & kFirst) {
+                convert_queries(item % C::QS, lw, lane);
+                __syncwarp();
+                if (lane == 0) sm100::mbar_arrive(sb + C::QFULL + 8 * (item & 1));
             }
-        } else {
-            // Tile t is copied once tile t - STG is done, and announced LAG tiles later, so that the
-            // tile before the one that is waited for can be in work.
-            constexpr int LAG = C::STG > 2 ? C::STG - 2 : 0;
-            for (int t = 0; t < T + LAG; ++t) {
-                if (t >= C::STG && t < T &&
-                    !sm100::mbar_wait(sb + C::EMPTY + 8 * (t % C::STG), (t / C::STG - 1) & 1)) { ok = false; break; }
-                put(t);
-                if (t >= LAG) {
-                    cp_async_wait<LAG>();
-                    announce(sb + C::FULL + 8 * ((t - LAG) % C::STG), lane);
-                }
-                if (aborted()) break;
-            }
+            if (t > 0 && !wait(sb + C::KFREE, (t - 1) & 1)) { ok = false; break; }
+            convert(raw, sb, seen, lw, lane);
+            announce(sb + C::KFULL, lane);
+            if (t > 0 && !wait(sb + C::VFREE, (t - 1) & 1)) { ok = false; break; }
+            convert(raw + C::RAW, sb + C::OP, seen, lw, lane);
+            announce(sb + C::VFULL, lane);
+            if (lane == 0) sm100::mbar_arrive(sb + C::EMPTY + 8 * (t % C::STG));
         }
-        cp_async_wait<0>();
         if (!ok) fail();
     }
 
     // ------------------------------------------------------------------ products
     __device__ __forceinline__ uint32_t k_image(int t) const { return F8 ? sb : sb + C::RING + (t % C::STG) * C::STAGE; }
     __device__ __forceinline__ uint32_t v_image(int t) const { return F8 ? sb + C::OP : k_image(t) + C::RAW; }
-    __device__ __forceinline__ uint32_t full_bar(int t) const { return sb + C::FULL + (F8 ? 0 : 8 * (t % C::STG)); }
+    __device__ __forceinline__ uint32_t full_bar(int t) const { return F8 ? sb + C::KFULL : sb + C::FULL + 8 * (t % C::STG); }
     static __device__ __forceinline__ uint32_t full_phase(int t) { return F8 ? t & 1 : (t / C::STG) & 1; }
 
     // Issued by one thread, in whatever order the operands come: scores of tile s, values of tile p.
@@ -326,7 +256,7 @@ struct TcKernel {
         using namespace sm100;
         constexpr uint32_t id_s = idesc16(!F8, 128, N, false, false), id_o = idesc16(!F8, D, N, true, true);
         int s = 0, p = 0;
-        uint64_t t0 = 0;
+        long long t0 = 0;
         bool ok = true;
         for (uint32_t idle = 0; p < T;) {
             if (s < T && s < p + 2 && mbar_test(full_bar(s), full_phase(s)) &&
@@ -338,7 +268,7 @@ struct TcKernel {
                     umma_bf16(tmem + N * (s & 1), smem_desc(k + (x >> 2) * C::HALF + (x & 3) * 32, 16, 1024, kSwizzle128),
                               smem_desc(q + (x >> 2) * C::QHALF + (x & 3) * 32, 16, 1024, kSwizzle128), id_s, x > 0);
                 umma_commit(sb + C::SFULL + 8 * (s & 1));
-                if constexpr (F8) umma_commit(sb + C::EMPTY);
+                if constexpr (F8) umma_commit(sb + C::KFREE);
                 ++s;
                 idle = 0;
                 continue;
@@ -360,13 +290,13 @@ struct TcKernel {
                     continue;
                 }
             }
-            if (idle++ == 0) t0 = globaltimer_ns();
-            if ((idle & 255u) == 0 && (aborted() || globaltimer_ns() - t0 > 2 * kWaitLimitNs)) { ok = false; break; }
+            if (idle++ == 0) t0 = clock64();
+            if ((idle & 255u) == 0 && (aborted() || clock64() - t0 > 4000000000ll)) { ok = false; break; }
         }
         if (!ok) fail();
         // nothing may still run on the tensor pipe when Tensor Memory is released
         umma_commit(sb + C::FIN);
-        mbar_wait(sb + C::FIN, 0);
+        wait(sb + C::FIN, 0);
     }
 
     // ------------------------------------------------------------------ softmax
@@ -430,6 +360,7 @@ struct TcKernel {
         const int tid = 32 * w + lane, key = tid;
         const uint32_t tl = tmem + ((uint32_t)(32 * w) << 16);
         float2* mrow = reinterpret_cast<float2*>(sm + C::MROW);   // (maximum + slack, maximum or 0)
+        float2* info = reinterpret_cast<float2*>(sm + C::RINFO);
         float* wred = reinterpret_cast<float*>(sm + C::WRED);
         float* frow = reinterpret_cast<float*>(sm + C::FROW);
         const float cap2 = P.softcap * kLog2e;
@@ -437,22 +368,27 @@ struct TcKernel {
         uint64_t pos = 0, neg = 0;
         bool bad = false;
         for (int t = 0; t < T; ++t) {
-            bad = bad || !mbar_wait(sb + C::MFULL + 8 * (t % C::MD), (t / C::MD) & 1);
-            bad = bad || !mbar_wait(sb + C::SFULL + 8 * (t & 1), (t >> 1) & 1);
-            if (t > 0) bad = bad || !mbar_wait(sb + C::PVDONE + 8 * ((t - 1) & 1), ((t - 1) >> 1) & 1);
+            bad = bad || !wait(sb + C::MFULL + 8 * (t % C::MD), (t / C::MD) & 1);
             const Meta mt = *meta(t);
             const bool first = mt.flags & kFirst, edge = mt.flags & kEdge;
             if (first) {
-                if (tid < N) mrow[tid] = make_float2(-INFINITY, 0.f);
+                if constexpr (F8) bad = bad || !wait(sb + C::QFULL + 8 * (mt.item & 1), (mt.item >> 1) & 1);
+                if (tid < N) {
+                    mrow[tid] = make_float2(-INFINITY, 0.f);
+                    float f = P.scale * (P.softcap > 0.f ? 2.f * kLog2e / P.softcap : kLog2e), slope = 0.f;
+                    if (F8) f *= (P.c.k_scale ? P.c.k_scale[mt.h] : 1.f) * reinterpret_cast<const float*>(sm + C::QF)[(mt.item % C::QS) * N + tid];
+                    if (P.slopes && tid < mt.rows) slope = P.slopes[mt.h * P.group + (mt.block * N + tid) % P.group] * kLog2e;
+                    info[tid] = make_float2(f, slope);   // scale of the raw products, bias per key
+                }
 #pragma unroll
                 for (int r = 0; r < N; ++r) l[r] = 0.f;
                 pos = neg = 0;
             }
+            bad = bad || !wait(sb + C::SFULL + 8 * (t & 1), (t >> 1) & 1);
             if (bar_any<1>(bad || aborted(), 128)) break;
             tc_fence_after();
             const bool ok = (reinterpret_cast<const uint32_t*>(sm + C::OKM + (t % C::MD) * 16)[w] >> lane) & 1;
             const bool mask = edge || !__all_sync(0xffffffffu, ok);
-            const float2* info = reinterpret_cast<const float2*>(sm + C::RINFO) + (mt.item % C::QS) * N;
             const uint32_t tS = tl + N * (t & 1), tO = tl + 2 * N + N * (mt.item & 1);
             const int j = mt.j0 + key;
 #pragma unroll
@@ -489,7 +425,10 @@ struct TcKernel {
 #pragma unroll
                     for (int i = c; i < c + 8; ++i) up = up || s[i] > mrow[32 * hb + i].x;
                 }
+                // the weights of the tile before, and O, are free
+                if (hb == 0 && t > 0) bad = bad || !wait(sb + C::PVDONE + 8 * ((t - 1) & 1), ((t - 1) >> 1) & 1);
                 if (bar_any<2>(up, 128)) {
+                    tc_fence_after();
                     // some row's maximum rises: the new one, and what the sums so far are worth in it
                     float mine = -INFINITY;
 #pragma unroll
@@ -546,8 +485,15 @@ struct TcKernel {
                     *reinterpret_cast<uint4*>(sm + C::PM + ((32 * hb + c) / 8) * (TOK * 16) + key * 16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                 }
             }
+            if (!F8 && !ok) {   // a value row that was not fetched
+                bad = bad || !wait(full_bar(t), full_phase(t));
+                uint8_t* v = sm + (v_image(t) - sb);
+#pragma unroll
+                for (int x = 0; x < D / 8; ++x)
+                    *reinterpret_cast<uint4*>(v + (x >> 3) * C::HALF + sm100::sw128_off(key, x & 7)) = make_uint4(0u, 0u, 0u, 0u);
+            }
             if (edge) {
-                bad = bad || !mbar_wait(F8 ? sb + C::VFULL : full_bar(t), F8 ? t & 1 : full_phase(t));
+                bad = bad || !wait(F8 ? sb + C::VFULL : full_bar(t), F8 ? t & 1 : full_phase(t));
                 sanitize(mt, t, ok, w, lane, pos, neg);
             }
             tc_fence_before();
@@ -558,7 +504,7 @@ struct TcKernel {
                 mbar_arrive(sb + C::PFULL);
             }
             if (mt.flags & kLast) {
-                bad = bad || !mbar_wait(sb + C::PVDONE + 8 * (t & 1), (t >> 1) & 1);
+                bad = bad || !wait(sb + C::PVDONE + 8 * (t & 1), (t >> 1) & 1);
                 tc_fence_after();
                 epilogue(mt, tO, l, pos, neg, w, lane);
                 tc_fence_before();
@@ -642,13 +588,19 @@ struct TcKernel {
         }
         if (warp == 0) sm100::tmem_alloc(sb + C::TMEM, C::TCOLS);
         if (tid == 32) {
-            for (int i = 0; i < C::NFULL; ++i) {
-                sm100::mbar_init(sb + C::FULL + 8 * i, C::LW);
-                sm100::mbar_init(sb + C::EMPTY + 8 * i, 1);
+            for (int i = 0; i < C::STG; ++i) {
+                sm100::mbar_init(sb + C::FULL + 8 * i, 1);
+                sm100::mbar_init(sb + C::EMPTY + 8 * i, F8 ? C::LW : 1);
             }
-            sm100::mbar_init(sb + C::VFULL, C::LW);
-            sm100::mbar_init(sb + C::VFREE, 1);
-            for (int i = 0; i < C::MD; ++i) sm100::mbar_init(sb + C::MFULL + 8 * i, C::LW);
+            for (int i = 0; i < C::MD; ++i) sm100::mbar_init(sb + C::MFULL + 8 * i, 1);
+            if (F8) {
+                sm100::mbar_init(sb + C::KFULL, C::LW);
+                sm100::mbar_init(sb + C::KFREE, 1);
+                sm100::mbar_init(sb + C::VFULL, C::LW);
+                sm100::mbar_init(sb + C::VFREE, 1);
+                sm100::mbar_init(sb + C::QFULL, C::LW);
+                sm100::mbar_init(sb + C::QFULL + 8, C::LW);
+            }
             for (int i = 0; i < 2; ++i) {
                 sm100::mbar_init(sb + C::SFULL + 8 * i, 1);
                 sm100::mbar_init(sb + C::SFREE + 8 * i, 4);
@@ -666,14 +618,18 @@ struct TcKernel {
         const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + C::TMEM);
         if (warp < 4) {
             softmax(tmem, warp, lane);
-        } else if (warp < 4 + C::LW) {
-            loader(w, warp - 4, lane);
-        } else if (lane == 0) {
-            issuer(tmem);
+        } else if (warp == 4) {
+            fetcher(w, lane);
+        } else if (warp == 5) {
+            if (lane == 0) issuer(tmem);
+        } else {
+            if constexpr (F8) converter(warp - 6, lane);
         }
         sm100::tc_fence_before();
         __syncthreads();
         sm100::tc_fence_after();
+        if (tid == 0 && aborted()) drain();
+        __syncwarp();
         if (warp == 0) sm100::tmem_dealloc(tmem, C::TCOLS);
     }
 };
@@ -686,15 +642,21 @@ __global__ void __launch_bounds__(Tc<D, TC, N>::THREADS, 1) attend_tc_kernel(con
 }
 
 template <int D, typename TC, int N>
-cudaError_t launch_tc(const Params& P, cudaStream_t stream) {
-    return launch_pair<D, __nv_bfloat16, TC, N>(attend_tc_kernel<D, TC, N>, Tc<D, TC, N>::THREADS, Tc<D, TC, N>::BYTES, P, stream);
+cudaError_t launch_tc(Params& P, cudaStream_t stream) {
+    typedef Tc<D, TC, N> C;
+    if (!make_maps<C>(P, D, (int)sizeof(TC), sizeof(TC) == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                      CU_TENSOR_MAP_DATA_TYPE_BFLOAT16))
+        return cudaErrorNotSupported;
+    return launch_pair<D, __nv_bfloat16, TC, N>(attend_tc_kernel<D, TC, N>, C::THREADS, C::BYTES, P, stream);
 }
 template <int D, int R>
-cudaError_t launch_simt(const Params& P, cudaStream_t stream) {
-    return launch_pair<D, float, float, R>(attend_simt_kernel<D, R>, Simt<D, R>::THREADS, Simt<D, R>::BYTES, P, stream);
+cudaError_t launch_simt(Params& P, cudaStream_t stream) {
+    typedef Simt<D, R> C;
+    if (!make_maps<C>(P, D, 4, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, CU_TENSOR_MAP_DATA_TYPE_FLOAT32)) return cudaErrorNotSupported;
+    return launch_pair<D, float, float, R>(attend_simt_kernel<D, R>, C::THREADS, C::BYTES, P, stream);
 }
 template <int D, typename T, typename TC>
-cudaError_t launch(const Params& P, cudaStream_t stream) {
+cudaError_t launch(Params& P, cudaStream_t stream) {
     const int rows = block_rows(sizeof(T) == 4, P.group * P.max_q);
     if constexpr (sizeof(T) == 4)
         return rows == 2 ? launch_simt<D, 2>(P, stream) : launch_simt<D, 8>(P, stream);

@@ -494,7 +494,8 @@ kda_status kda_kv_decode(const void* q, int64_t q_stride, kda_dtype dt, const kd
     P.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kda::attend::header_bytes());
     const cudaError_t err = KDA_KV_DISPATCH(kda::attend::launch, cache->D, dt, cache->dt, P,
                                             reinterpret_cast<cudaStream_t>(stream));
-    return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    // strides beyond 2^40 bytes have no TMA map
+    return err == cudaSuccess ? KDA_OK : err == cudaErrorNotSupported ? KDA_ERR_UNSUPPORTED : KDA_ERR_CUDA;
 }
 
 #ifdef KDA_TRACE
