@@ -89,6 +89,13 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
     return done != 0;
 }
 
+// true in one lane of the warp, the same each time
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
     uint32_t r[8];
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -251,51 +258,70 @@ struct TcKernel {
     __device__ __forceinline__ uint32_t full_bar(int t) const { return F8 ? sb + C::KFULL : sb + C::FULL + 8 * (t % C::STG); }
     static __device__ __forceinline__ uint32_t full_phase(int t) { return F8 ? t & 1 : (t / C::STG) & 1; }
 
-    // Issued by one thread, in whatever order the operands come: scores of tile s, values of tile p.
+    // Scores of tile s, values of tile p, in whatever order the operands come.  The whole warp walks
+    // through (its decisions are votes, so that descriptors stay in uniform registers), one lane issues.
     __device__ __forceinline__ void issuer(uint32_t tmem) {
         using namespace sm100;
         constexpr uint32_t id_s = idesc16(!F8, 128, N, false, false), id_o = idesc16(!F8, D, N, true, true);
-        int s = 0, p = 0;
+        const uint64_t k0 = smem_desc(sb + (F8 ? 0 : C::RING), 16, 1024, kSwizzle128), q0 = smem_desc(sb + C::Q, 16, 1024, kSwizzle128);
+        const uint64_t v0 = smem_desc(sb + (F8 ? C::OP : C::RING + C::RAW), C::HALF, 1024, kSwizzle128);
+        const uint64_t p0 = smem_desc(sb + C::PM, 128, TOK * 16, 0);
+        int s = 0, p = 0, ss = 0, ps = 0;   // tiles, and their stages
+        uint32_t sp = 0;                    // phase of tile s's stage
+        int qslot = -1, item = -1;          // of tile s, of tile p
         long long t0 = 0;
         bool ok = true;
         for (uint32_t idle = 0; p < T;) {
-            if (s < T && s < p + 2 && mbar_test(full_bar(s), full_phase(s)) &&
-                (s < 2 || mbar_test(sb + C::SFREE + 8 * (s & 1), ((s >> 1) - 1) & 1))) {
+            bool go = s < T && s < p + 2 && mbar_test(F8 ? sb + C::KFULL : sb + C::FULL + 8 * ss, F8 ? s & 1 : sp) &&
+                      (s < 2 || mbar_test(sb + C::SFREE + 8 * (s & 1), ((s >> 1) - 1) & 1));
+            if (__all_sync(0xffffffffu, go)) {
                 tc_fence_after();
-                const uint32_t q = sb + C::Q + (meta(s)->item % C::QS) * C::QB, k = k_image(s);
+                if (__any_sync(0xffffffffu, meta(s)->flags & kFirst)) qslot = qslot + 1 == C::QS ? 0 : qslot + 1;
+                const uint64_t k = k0 + (F8 ? 0 : (uint32_t)(ss * C::STAGE) >> 4), q = q0 + ((uint32_t)(qslot * C::QB) >> 4);
+                if (elect_one()) {
 #pragma unroll
-                for (int x = 0; x < D / 16; ++x)
-                    umma_bf16(tmem + N * (s & 1), smem_desc(k + (x >> 2) * C::HALF + (x & 3) * 32, 16, 1024, kSwizzle128),
-                              smem_desc(q + (x >> 2) * C::QHALF + (x & 3) * 32, 16, 1024, kSwizzle128), id_s, x > 0);
-                umma_commit(sb + C::SFULL + 8 * (s & 1));
-                if constexpr (F8) umma_commit(sb + C::KFREE);
+                    for (int x = 0; x < D / 16; ++x)
+                        umma_bf16(tmem + N * (s & 1), k + (((x >> 2) * C::HALF + (x & 3) * 32) >> 4),
+                                  q + (((x >> 2) * C::QHALF + (x & 3) * 32) >> 4), id_s, x > 0);
+                    umma_commit(sb + C::SFULL + 8 * (s & 1));
+                    if constexpr (F8) umma_commit(sb + C::KFREE);
+                }
+                __syncwarp();
                 ++s;
+                if (++ss == C::STG) { ss = 0; sp ^= 1; }
                 idle = 0;
                 continue;
             }
-            if (p < s && mbar_test(sb + C::PFULL, p & 1) && (!F8 || mbar_test(sb + C::VFULL, p & 1))) {
-                const int item = meta(p)->item;
-                const bool first = meta(p)->flags & kFirst;
-                if (!first || item < 2 || mbar_test(sb + C::OFREE + 8 * (item & 1), ((item >> 1) - 1) & 1)) {
+            go = p < s && mbar_test(sb + C::PFULL, p & 1) && (!F8 || mbar_test(sb + C::VFULL, p & 1));
+            if (__all_sync(0xffffffffu, go)) {
+                const bool first = __any_sync(0xffffffffu, meta(p)->flags & kFirst);
+                const int it = item + (first ? 1 : 0);
+                go = !first || it < 2 || mbar_test(sb + C::OFREE + 8 * (it & 1), ((it >> 1) - 1) & 1);
+                if (__all_sync(0xffffffffu, go)) {
+                    item = it;
                     tc_fence_after();
-                    const uint32_t v = v_image(p);
+                    const uint64_t v = v0 + (F8 ? 0 : (uint32_t)(ps * C::STAGE) >> 4);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int x = 0; x < TOK / 16; ++x)
-                        umma_bf16(tmem + 2 * N + N * (item & 1), smem_desc(v + x * 2048, C::HALF, 1024, kSwizzle128),
-                                  smem_desc(sb + C::PM + x * 256, 128, TOK * 16, 0), id_o, x > 0 || !first);
-                    umma_commit(sb + C::PVDONE + 8 * (p & 1));
-                    umma_commit(F8 ? sb + C::VFREE : sb + C::EMPTY + 8 * (p % C::STG));
+                        for (int x = 0; x < TOK / 16; ++x)
+                            umma_bf16(tmem + 2 * N + N * (it & 1), v + (x * 2048 >> 4), p0 + (x * 256 >> 4), id_o, x > 0 || !first);
+                        umma_commit(sb + C::PVDONE + 8 * (p & 1));
+                        umma_commit(F8 ? sb + C::VFREE : sb + C::EMPTY + 8 * ps);
+                    }
+                    __syncwarp();
                     ++p;
+                    if (++ps == C::STG) ps = 0;
                     idle = 0;
                     continue;
                 }
             }
             if (idle++ == 0) t0 = clock64();
-            if ((idle & 255u) == 0 && (aborted() || clock64() - t0 > 4000000000ll)) { ok = false; break; }
+            if ((idle & 255u) == 0 && __any_sync(0xffffffffu, aborted() || clock64() - t0 > 4000000000ll)) { ok = false; break; }
         }
         if (!ok) fail();
         // nothing may still run on the tensor pipe when Tensor Memory is released
-        umma_commit(sb + C::FIN);
+        if (elect_one()) umma_commit(sb + C::FIN);
+        __syncwarp();
         wait(sb + C::FIN, 0);
     }
 
@@ -398,36 +424,49 @@ struct TcKernel {
                 if constexpr (WD == 32) tmem_ld32(tS + 32 * hb, s);
                 else tmem_ld16(tS, s);
                 tmem_wait_ld();
-                bool up = false;
+                uint32_t up = 0;   // counted without branches
                 int tok = (mt.block * N + 32 * hb) / P.group, left = (tok + 1) * P.group - (mt.block * N + 32 * hb);
 #pragma unroll
                 for (int c = 0; c < WD; c += 8) {
                     if (32 * hb + c >= mt.rows) break;
+                    float2 in[8];
+                    float top[8];
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2) {   // two rows a load, the same for all lanes
+                        const float4 u = *reinterpret_cast<const float4*>(info + 32 * hb + c + i);
+                        const float4 m = *reinterpret_cast<const float4*>(mrow + 32 * hb + c + i);
+                        in[i] = make_float2(u.x, u.y);
+                        in[i + 1] = make_float2(u.z, u.w);
+                        top[i] = m.x;
+                        top[i + 1] = m.z;
+                    }
                     if (P.softcap > 0.f) {
                         // cap tanh(x / cap) = cap (1 - 2 / (1 + e^{2 x / cap})): off by up to 2^-21 cap, far below the
                         // weights' own rounding
 #pragma unroll
-                        for (int i = c; i < c + 8; ++i)
-                            s[i] = cap2 - 2.f * cap2 * rcp(1.f + ex2(s[i] * info[32 * hb + i].x));
+                        for (int i = 0; i < 8; ++i) s[c + i] = cap2 - 2.f * cap2 * rcp(1.f + ex2(s[c + i] * in[i].x));
                     } else {
 #pragma unroll
-                        for (int i = c; i < c + 8; ++i) s[i] *= info[32 * hb + i].x;
+                        for (int i = 0; i < 8; ++i) s[c + i] *= in[i].x;
                     }
                     if (P.slopes || mask) {
 #pragma unroll
-                        for (int i = c; i < c + 8; ++i) {
+                        for (int i = 0; i < 8; ++i) {
                             const int p = mt.pos0 + tok;
-                            if (P.slopes) s[i] += info[32 * hb + i].y * (float)(j - p);
-                            if (mask && !(ok && j <= p && j >= first_key(P, mt.start, p))) s[i] = -INFINITY;
-                            if (--left == 0) { ++tok; left = P.group; }
+                            s[c + i] += in[i].y * (float)(j - p);   // no bias: a slope of 0
+                            const bool seen = ok & (j <= p) & (j >= mt.start) & (P.window <= 0 | (int64_t)p - j < P.window);
+                            s[c + i] = seen ? s[c + i] : -INFINITY;
+                            const bool over = --left == 0;
+                            tok += over;
+                            left = over ? P.group : left;
                         }
                     }
 #pragma unroll
-                    for (int i = c; i < c + 8; ++i) up = up || s[i] > mrow[32 * hb + i].x;
+                    for (int i = 0; i < 8; ++i) up |= s[c + i] > top[i];
                 }
                 // the weights of the tile before, and O, are free
                 if (hb == 0 && t > 0) bad = bad || !wait(sb + C::PVDONE + 8 * ((t - 1) & 1), ((t - 1) >> 1) & 1);
-                if (bar_any<2>(up, 128)) {
+                if (bar_any<2>(up != 0, 128)) {
                     tc_fence_after();
                     // some row's maximum rises: the new one, and what the sums so far are worth in it
                     float mine = -INFINITY;
@@ -477,7 +516,8 @@ struct TcKernel {
                     uint32_t pk[4];
 #pragma unroll
                     for (int i = 0; i < 8; i += 2) {
-                        const float a = ex2(s[c + i] - mrow[32 * hb + c + i].y), b = ex2(s[c + i + 1] - mrow[32 * hb + c + i + 1].y);
+                        const float4 m = *reinterpret_cast<const float4*>(mrow + 32 * hb + c + i);
+                        const float a = ex2(s[c + i] - m.y), b = ex2(s[c + i + 1] - m.w);
                         l[32 * hb + c + i] += a;
                         l[32 * hb + c + i + 1] += b;
                         pk[i / 2] = F8 ? pack_half2(a, b) : pack_bf16x2(a, b);
@@ -621,7 +661,7 @@ struct TcKernel {
         } else if (warp == 4) {
             fetcher(w, lane);
         } else if (warp == 5) {
-            if (lane == 0) issuer(tmem);
+            issuer(tmem);
         } else {
             if constexpr (F8) converter(warp - 6, lane);
         }
