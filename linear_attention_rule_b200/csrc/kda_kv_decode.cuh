@@ -140,15 +140,15 @@ __device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap* map, int x
         "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
         ::"r"(dst), "l"(map), "r"(x), "r"(head), "r"(token), "r"(bar) : "memory");
 }
-// Barrier ID of `count` threads that tells all of them whether `p` holds for any.
-template <int ID> __device__ __forceinline__ bool bar_any(bool p, uint32_t count) {
+// Barrier `id` of `count` threads that tells all of them whether `p` holds for any.
+__device__ __forceinline__ bool bar_any(uint32_t id, bool p, uint32_t count) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred a, b;\n\t"
         "setp.ne.u32 a, %1, 0;\n\t"
         "barrier.cta.red.or.pred b, %2, %3, a;\n\t"
         "selp.u32 %0, 1, 0, b;\n\t}"
-        : "=r"(r) : "r"((uint32_t)p), "n"(ID), "r"(count) : "memory");
+        : "=r"(r) : "r"((uint32_t)p), "r"(id), "r"(count) : "memory");
     return r != 0;
 }
 
@@ -161,7 +161,8 @@ struct Meta {
     int32_t all_lo;      // keys all_lo .. pos0 are seen by every token
     int32_t item;        // count of items in this stretch
     int32_t part;        // where the item's triple goes: -1 (finished here) or a slot of P.partial
-    int32_t pad[3];
+    int32_t tok0, left0; // token of the block's first row, and how many rows of the block are of that token
+    int32_t pad;
 };
 static_assert(sizeof(Meta) == 64, "laid out in shared memory");
 enum : int32_t { kFirst = 1, kLast = 2, kEdge = 4 };   // first, last tile of the item here; not all keys seen by all
@@ -275,6 +276,8 @@ struct Walk {
         m->start = s.start;
         m->all_lo = all_lo;
         m->item = item;
+        m->tok0 = block * ROWS / P.group;
+        m->left0 = (m->tok0 + 1) * P.group - block * ROWS;
         m->part = starts && ends ? -1 : 2 * (int)blockIdx.x + (starts ? 1 : 0);
     }
     __device__ __forceinline__ void tell_join(Split* to) const {

@@ -80,7 +80,7 @@ struct SimtKernel {
         bool bad = false;
         for (int t = 0; t < T; ++t) {
             bad = bad || !wait(sb + C::FULL + 8 * (t % C::STG), (t / C::STG) & 1);
-            if (bar_any<1>(bad || aborted(), NT)) break;
+            if (bar_any(1, bad || aborted(), NT)) break;
             const Meta mt = *meta(t);
             const uint32_t* okm = reinterpret_cast<const uint32_t*>(sm + C::OKM + (t % C::MD) * 16);
             bool all = true;   // all keys there

@@ -9,8 +9,9 @@
 // as one 16-byte chunk per 8 rows (P MN-major without swizzle, free of bank conflicts).  Only the
 // running maximum is shared, and the tile that raises it by more than 2^8 is rare (kSlack).
 //
-// Warps: 0-3 softmax and epilogue (TMEM lanes 32 w ..), 4 fetches tiles, 5 issues the products, with
-// an e4m3 cache 6-13 convert.  S and O are double-buffered in TMEM, so the product of the next tile
+// Warps: 4 for softmax and epilogue (TMEM lanes 32 w ..) for every 16 rows (8 with 32 and 64), which
+// share nothing but keys and values; then one that fetches tiles, one that issues the products, and
+// with an e4m3 cache those that convert.  S and O are double-buffered in TMEM, so the product of the next tile
 // runs during the softmax of this one and the next item starts during the epilogue of the last.
 //
 // bf16: tiles land in the operand images directly (TMA's 128-byte swizzle is the images').
@@ -31,8 +32,10 @@ template <int D_, typename TC, int N>
 struct Tc {
     static constexpr int D = D_;
     static constexpr bool F8 = sizeof(TC) == 1;
-    static constexpr int TOK = 128, LW = F8 ? 8 : 0, RPW = F8 ? TOK / LW : TOK;   // converting warps, rows of each
-    static constexpr int THREADS = 32 * (6 + LW);
+    static constexpr int TOK = 128;
+    static constexpr int SW = N >= 32 ? 8 : 4, RW = N / (SW / 4);             // softmax warps, rows of four of them
+    static constexpr int LW = F8 ? (N >= 32 ? 4 : 8) : 0, RPW = F8 ? TOK / LW : TOK;   // converting warps, keys of each
+    static constexpr int THREADS = 32 * (SW + 2 + LW);
     static constexpr int ROWB = D * (int)sizeof(TC), CPR = ROWB / 16;  // a cache row
     static constexpr int OP = TOK * D * 2;                             // an operand image: D / 64 halves of 128-byte rows
     static constexpr int HALF = TOK * 128, QHALF = N * 128;
@@ -52,7 +55,7 @@ struct Tc {
     static constexpr int qslots(int stg) { return stg + (F8 ? 1 : 0); }
     static constexpr int metas(int stg) { return stg + 2; }
     static constexpr int misc(int stg) {
-        return metas(stg) * 64 + metas(stg) * 16 + qslots(stg) * N * 4 + N * 8 + N * 8 + 4 * N * 4 + N * 4 + 8 * (2 * stg + metas(stg) + 18) + 16;
+        return metas(stg) * 64 + metas(stg) * 16 + qslots(stg) * N * 4 + N * 8 + N * 8 + 4 * N * 4 + N * 4 + 8 * (2 * stg + metas(stg) + 18) + 32;
     }
     static constexpr int total(int stg) { return FIXED + stg * STAGE + qslots(stg) * QB + PB + misc(stg); }
     static constexpr int most(int stg) { return stg > 2 && total(stg) > kMaxSmem ? most(stg - 1) : stg; }
@@ -68,8 +71,8 @@ struct Tc {
     // barriers
     static constexpr int FULL = BAR, EMPTY = FULL + 8 * STG, MFULL = EMPTY + 8 * STG, KFULL = MFULL + 8 * MD, KFREE = KFULL + 8,
                          VFULL = KFREE + 8, VFREE = VFULL + 8, QFULL = VFREE + 8, SFULL = QFULL + 16, SFREE = SFULL + 16,
-                         PFULL = SFREE + 16, PVDONE = PFULL + 8, OFREE = PVDONE + 16, FIN = OFREE + 16, TMEM = FIN + 8, ABORT = TMEM + 4;
-    static_assert(ABORT + 4 <= BYTES, "misc");
+                         PFULL = SFREE + 16, PVDONE = PFULL + 8, OFREE = PVDONE + 16, FIN = OFREE + 16, TMEM = FIN + 8, ABORT = TMEM + 4, BITS = ABORT + 4;
+    static_assert(BITS + 16 <= BYTES, "misc");
     static constexpr int TCOLS = 4 * N;   // S twice, O twice
 };
 
@@ -234,7 +237,7 @@ struct TcKernel {
             ok = !aborted() && wait(sb + C::FULL + 8 * (t % C::STG), (t / C::STG) & 1);
             if (!ok) break;
             const uint32_t raw = sb + C::RING + (t % C::STG) * C::STAGE;
-            const uint32_t seen = reinterpret_cast<const uint16_t*>(sm + C::OKM + (t % C::MD) * 16)[lw];
+            const uint32_t seen = reinterpret_cast<const uint32_t*>(sm + C::OKM + (t % C::MD) * 16)[lw * C::RPW / 32] >> (lw * C::RPW % 32);
             const int item = meta(t)->item;
             if (meta(t)->flags & kFirst) {
                 convert_queries(item % C::QS, lw, lane);
@@ -326,17 +329,23 @@ struct TcKernel {
     }
 
     // ------------------------------------------------------------------ softmax
+    // Four warps have RW rows: wq is the warp among them, row0 the first row, bar their barrier.
     // This thread's channel of O^T: TMEM lanes are channels, with D = 64 the first 16 of each 32.
-    static __device__ __forceinline__ int channel(int w, int lane) { return D == 128 ? 32 * w + lane : lane < 16 ? 16 * w + lane : -1; }
+    static __device__ __forceinline__ int channel(int wq, int lane) { return D == 128 ? 32 * wq + lane : lane < 16 ? 16 * wq + lane : -1; }
     __device__ __forceinline__ static bool finite16(uint32_t x) { return F8 ? (x & 0x7c00u) != 0x7c00u : (x & 0x7f80u) != 0x7f80u; }
+    __device__ __forceinline__ bool sees(const Meta& mt, int j, int p) const {
+        return (j <= p) & (j >= mt.start) & ((P.window <= 0) | ((int64_t)p - j < P.window));
+    }
 
     // Keys that some tokens see and some do not take part in the product for all (with weight 0
     // for those that do not see them), which a NaN or infinity among their values would break: such
     // elements are taken out of the image, and the channel's rows that see them noted in pos / neg.
-    __device__ __forceinline__ void sanitize(const Meta& mt, int t, bool ok, int w, int lane, uint64_t& pos, uint64_t& neg) {
+    // All softmax warps.
+    __device__ __forceinline__ void sanitize(const Meta& mt, int t, bool ok, int wq, int lane, int row0, uint32_t& pos, uint32_t& neg) {
+        constexpr uint32_t ALL = 32 * C::SW;
         uint8_t* v = sm + (v_image(t) - sb);
-        const int key = 32 * w + lane, j = mt.j0 + key;
-        bool bad = false;
+        const int key = 32 * wq + lane, j = mt.j0 + key;
+        uint32_t bad = 0;
         if (ok && (j > mt.pos0 || j < mt.all_lo)) {
 #pragma unroll
             for (int h = 0; h < D / 64; ++h)
@@ -345,196 +354,198 @@ struct TcKernel {
                     const uint4 u = *reinterpret_cast<const uint4*>(v + h * C::HALF + sm100::sw128_off(key, ch));
                     const uint32_t a[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) bad = bad || !finite16(a[x] & 0xffffu) || !finite16(a[x] >> 16);
+                    for (int x = 0; x < 4; ++x) bad |= !finite16(a[x] & 0xffffu) | !finite16(a[x] >> 16);
                 }
         }
-        if (!bar_any<1>(bad, 128)) return;
-        volatile uint32_t* bits = reinterpret_cast<volatile uint32_t*>(sm + C::WRED);
-        const uint32_t mine = __ballot_sync(0xffffffffu, bad);
-        if (lane == 0) bits[w] = mine;
-        sm100::bar_sync_fixed<1>(128);
-        const int d = channel(w, lane);
-        for (int x = 0; x < 4; ++x)
-            for (uint32_t m = bits[x]; m; m &= m - 1) {
-                const int k = 32 * x + __ffs(m) - 1;
-                if (d < 0) continue;
-                uint16_t* e = reinterpret_cast<uint16_t*>(v + (d >> 6) * C::HALF + sm100::sw128_off(k, (d & 63) >> 3) + 2 * (d & 7));
-                const uint32_t val = *e;
-                if (finite16(val)) continue;
-                *e = 0;
-                const bool nan = F8 ? (val & 0x3ffu) != 0 : (val & 0x7fu) != 0, minus = val & 0x8000u;
-                for (int r = 0; r < mt.rows; ++r) {
-                    const int p = mt.pos0 + (mt.block * N + r) / P.group, jk = mt.j0 + k;
-                    if (jk > p || jk < first_key(P, mt.start, p)) continue;
-                    if (nan || !minus) pos |= 1ull << r;
-                    if (nan || minus) neg |= 1ull << r;
+        if (!bar_any(3, bad != 0, ALL)) return;
+        volatile uint32_t* bits = reinterpret_cast<volatile uint32_t*>(sm + C::BITS);
+        const uint32_t mine = __ballot_sync(0xffffffffu, bad != 0);
+        if (lane == 0) bits[wq] = mine;   // the same of both groups of warps
+        sm100::named_bar(3, ALL);
+        const int d = channel(wq, lane);
+        auto element = [&](int k) {
+            return reinterpret_cast<uint16_t*>(v + (d >> 6) * C::HALF + sm100::sw128_off(k, (d & 63) >> 3) + 2 * (d & 7));
+        };
+        if (d >= 0)
+            for (int x = 0; x < 4; ++x)
+                for (uint32_t m = bits[x]; m; m &= m - 1) {
+                    const int k = 32 * x + __ffs(m) - 1;
+                    const uint32_t val = *element(k);
+                    if (finite16(val)) continue;
+                    const bool nan = F8 ? (val & 0x3ffu) != 0 : (val & 0x7fu) != 0, minus = val & 0x8000u;
+                    for (int r = 0; r < C::RW && row0 + r < mt.rows; ++r) {
+                        if (!sees(mt, mt.j0 + k, mt.pos0 + (mt.block * N + row0 + r) / P.group)) continue;
+                        if (nan || !minus) pos |= 1u << r;
+                        if (nan || minus) neg |= 1u << r;
+                    }
                 }
-            }
-        sm100::bar_sync_fixed<1>(128);   // the list has been read
-    }
-
-    // (out - weighted sum, in fp32) of row r: what sanitize has noted
-    static __device__ __forceinline__ float poisoned(float x, int r, uint64_t pos, uint64_t neg) {
-        if ((pos >> r) & 1) x += INFINITY;
-        if ((neg >> r) & 1) x -= INFINITY;
-        return x;
+        sm100::named_bar(3, ALL);   // all have read
+        if (d >= 0 && row0 == 0)
+            for (int x = 0; x < 4; ++x)
+                for (uint32_t m = bits[x]; m; m &= m - 1) {
+                    uint16_t* e = element(32 * x + __ffs(m) - 1);
+                    if (!finite16(*e)) *e = 0;
+                }
+        sm100::named_bar(3, ALL);   // the list may be written again
     }
 
     __device__ __forceinline__ void softmax(uint32_t tmem, int w, int lane) {
         using namespace sm100;
-        constexpr int WD = N < 32 ? N : 32, HB = N / WD;   // rows in registers at a time
-        const int tid = 32 * w + lane, key = tid;
-        const uint32_t tl = tmem + ((uint32_t)(32 * w) << 16);
-        float2* mrow = reinterpret_cast<float2*>(sm + C::MROW);   // (maximum + slack, maximum or 0)
-        float2* info = reinterpret_cast<float2*>(sm + C::RINFO);
-        float* wred = reinterpret_cast<float*>(sm + C::WRED);
-        float* frow = reinterpret_cast<float*>(sm + C::FROW);
+        constexpr int RW = C::RW;
+        const int wq = w & 3, row0 = (w >> 2) * RW, tid = 32 * wq + lane, key = tid;
+        const uint32_t bar = 1 + (w >> 2), tl = tmem + ((uint32_t)(32 * wq) << 16);
+        float2* mrow = reinterpret_cast<float2*>(sm + C::MROW) + row0;   // (maximum + slack, maximum or 0)
+        float2* info = reinterpret_cast<float2*>(sm + C::RINFO) + row0;
+        float* wred = reinterpret_cast<float*>(sm + C::WRED) + row0;
+        float* frow = reinterpret_cast<float*>(sm + C::FROW) + row0;
         const float cap2 = P.softcap * kLog2e;
-        float l[N];
-        uint64_t pos = 0, neg = 0;
+        float l[RW];
+        uint32_t pos = 0, neg = 0;
         bool bad = false;
         for (int t = 0; t < T; ++t) {
             bad = bad || !wait(sb + C::MFULL + 8 * (t % C::MD), (t / C::MD) & 1);
             const Meta mt = *meta(t);
             const bool first = mt.flags & kFirst, edge = mt.flags & kEdge;
+            const int rows = mt.rows - row0;   // of these warps; maybe none
             if (first) {
                 if constexpr (F8) bad = bad || !wait(sb + C::QFULL + 8 * (mt.item & 1), (mt.item >> 1) & 1);
-                if (tid < N) {
+                if (tid < RW) {
                     mrow[tid] = make_float2(-INFINITY, 0.f);
                     float f = P.scale * (P.softcap > 0.f ? 2.f * kLog2e / P.softcap : kLog2e), slope = 0.f;
-                    if (F8) f *= (P.c.k_scale ? P.c.k_scale[mt.h] : 1.f) * reinterpret_cast<const float*>(sm + C::QF)[(mt.item % C::QS) * N + tid];
-                    if (P.slopes && tid < mt.rows) slope = P.slopes[mt.h * P.group + (mt.block * N + tid) % P.group] * kLog2e;
+                    if (F8) f *= (P.c.k_scale ? P.c.k_scale[mt.h] : 1.f) * reinterpret_cast<const float*>(sm + C::QF)[(mt.item % C::QS) * N + row0 + tid];
+                    if (P.slopes && tid < rows) slope = P.slopes[mt.h * P.group + (mt.block * N + row0 + tid) % P.group] * kLog2e;
                     info[tid] = make_float2(f, slope);   // scale of the raw products, bias per key
                 }
 #pragma unroll
-                for (int r = 0; r < N; ++r) l[r] = 0.f;
+                for (int r = 0; r < RW; ++r) l[r] = 0.f;
                 pos = neg = 0;
             }
             bad = bad || !wait(sb + C::SFULL + 8 * (t & 1), (t >> 1) & 1);
-            if (bar_any<1>(bad || aborted(), 128)) break;
+            if (bar_any(bar, bad || aborted(), 128)) break;
             tc_fence_after();
-            const bool ok = (reinterpret_cast<const uint32_t*>(sm + C::OKM + (t % C::MD) * 16)[w] >> lane) & 1;
+            const bool ok = (reinterpret_cast<const uint32_t*>(sm + C::OKM + (t % C::MD) * 16)[wq] >> lane) & 1;
             const bool mask = edge || !__all_sync(0xffffffffu, ok);
-            const uint32_t tS = tl + N * (t & 1), tO = tl + 2 * N + N * (mt.item & 1);
+            const uint32_t tS = tl + N * (t & 1) + row0, tO = tl + 2 * N + N * (mt.item & 1) + row0;
             const int j = mt.j0 + key;
-#pragma unroll
-            for (int hb = 0; hb < HB; ++hb) {
-                if (32 * hb >= mt.rows) break;
-                float s[WD];
-                if constexpr (WD == 32) tmem_ld32(tS + 32 * hb, s);
+            float s[RW];
+            if (rows > 0) {
+                if constexpr (RW == 32) tmem_ld32(tS, s);
                 else tmem_ld16(tS, s);
                 tmem_wait_ld();
-                uint32_t up = 0;   // counted without branches
-                int tok = (mt.block * N + 32 * hb) / P.group, left = (tok + 1) * P.group - (mt.block * N + 32 * hb);
+            }
+            uint32_t up = 0;   // counted without branches
+            int tok = mt.tok0, left = mt.left0;
+            if ((P.slopes || mask) && row0) {
+                tok = (mt.block * N + row0) / P.group;
+                left = (tok + 1) * P.group - (mt.block * N + row0);
+            }
 #pragma unroll
-                for (int c = 0; c < WD; c += 8) {
-                    if (32 * hb + c >= mt.rows) break;
-                    float2 in[8];
-                    float top[8];
+            for (int c = 0; c < RW; c += 8) {
+                if (c >= rows) break;
+                float2 in[8];
+                float top[8];
 #pragma unroll
-                    for (int i = 0; i < 8; i += 2) {   // two rows a load, the same for all lanes
-                        const float4 u = *reinterpret_cast<const float4*>(info + 32 * hb + c + i);
-                        const float4 m = *reinterpret_cast<const float4*>(mrow + 32 * hb + c + i);
-                        in[i] = make_float2(u.x, u.y);
-                        in[i + 1] = make_float2(u.z, u.w);
-                        top[i] = m.x;
-                        top[i + 1] = m.z;
-                    }
-                    if (P.softcap > 0.f) {
-                        // cap tanh(x / cap) = cap (1 - 2 / (1 + e^{2 x / cap})): off by up to 2^-21 cap, far below the
-                        // weights' own rounding
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) s[c + i] = cap2 - 2.f * cap2 * rcp(1.f + ex2(s[c + i] * in[i].x));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) s[c + i] *= in[i].x;
-                    }
-                    if (P.slopes || mask) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int p = mt.pos0 + tok;
-                            s[c + i] += in[i].y * (float)(j - p);   // no bias: a slope of 0
-                            const bool seen = ok & (j <= p) & (j >= mt.start) & (P.window <= 0 | (int64_t)p - j < P.window);
-                            s[c + i] = seen ? s[c + i] : -INFINITY;
-                            const bool over = --left == 0;
-                            tok += over;
-                            left = over ? P.group : left;
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) up |= s[c + i] > top[i];
+                for (int i = 0; i < 8; i += 2) {   // two rows a load, the same for all lanes
+                    const float4 u = *reinterpret_cast<const float4*>(info + c + i);
+                    const float4 m = *reinterpret_cast<const float4*>(mrow + c + i);
+                    in[i] = make_float2(u.x, u.y);
+                    in[i + 1] = make_float2(u.z, u.w);
+                    top[i] = m.x;
+                    top[i + 1] = m.z;
                 }
-                // the weights of the tile before, and O, are free
-                if (hb == 0 && t > 0) bad = bad || !wait(sb + C::PVDONE + 8 * ((t - 1) & 1), ((t - 1) >> 1) & 1);
-                if (bar_any<2>(up != 0, 128)) {
-                    tc_fence_after();
-                    // some row's maximum rises: the new one, and what the sums so far are worth in it
-                    float mine = -INFINITY;
+                if (P.softcap > 0.f) {
+                    // cap tanh(x / cap) = cap (1 - 2 / (1 + e^{2 x / cap})): off by up to 2^-21 cap, far below the
+                    // weights' own rounding
 #pragma unroll
-                    for (int c = 0; c < WD; c += 8) {
-                        if (32 * hb + c >= mt.rows) break;
+                    for (int i = 0; i < 8; ++i) s[c + i] = cap2 - 2.f * cap2 * rcp(1.f + ex2(s[c + i] * in[i].x));
+                } else {
 #pragma unroll
-                        for (int i = c; i < c + 8; ++i) {
-                            const float x = warp_max(s[i]);
-                            if (lane == i) mine = x;
-                        }
+                    for (int i = 0; i < 8; ++i) s[c + i] *= in[i].x;
+                }
+                if (P.slopes || mask) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int p = mt.pos0 + tok;
+                        s[c + i] += in[i].y * (float)(j - p);   // no bias: a slope of 0
+                        s[c + i] = ok & sees(mt, j, p) ? s[c + i] : -INFINITY;
+                        const bool over = --left == 0;
+                        tok += over;
+                        left = over ? P.group : left;
                     }
-                    if (lane < WD) wred[w * N + 32 * hb + lane] = mine;
-                    bar_sync_fixed<1>(128);
-                    if (tid < WD) {
-                        const int r = 32 * hb + tid;
-                        const float top = fmaxf(fmaxf(wred[r], wred[N + r]), fmaxf(wred[2 * N + r], wred[3 * N + r]));
-                        const float2 old = mrow[r];
-                        float f = 1.f;
-                        if (top > old.x) {
-                            f = old.x == -INFINITY ? 0.f : ex2(old.y - top);
-                            mrow[r] = make_float2(top + kSlack, top);
-                        }
-                        frow[r] = f;
-                    }
-                    bar_sync_fixed<1>(128);
+                }
 #pragma unroll
-                    for (int c = 0; c < WD; c += 8) {
-                        if (32 * hb + c >= mt.rows) break;
-                        if (first) continue;   // nothing summed yet
+                for (int i = 0; i < 8; ++i) up |= s[c + i] > top[i];
+            }
+            // the weights of the tile before, and O, are free
+            if (t > 0) bad = bad || !wait(sb + C::PVDONE + 8 * ((t - 1) & 1), ((t - 1) >> 1) & 1);
+            if (bar_any(bar, up != 0, 128)) {
+                // some row's maximum rises: the new one, and what the sums so far are worth in it
+                tc_fence_after();
+                float mine = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < RW; c += 8) {
+                    if (c >= rows) break;
+#pragma unroll
+                    for (int i = c; i < c + 8; ++i) {
+                        const float x = warp_max(s[i]);
+                        if (lane == i) mine = x;
+                    }
+                }
+                if (lane < RW) wred[wq * N + lane] = mine;
+                named_bar(bar, 128);
+                if (tid < RW) {
+                    const float top = fmaxf(fmaxf(wred[tid], wred[N + tid]), fmaxf(wred[2 * N + tid], wred[3 * N + tid]));
+                    const float2 old = mrow[tid];
+                    float f = 1.f;
+                    if (top > old.x) {
+                        f = old.x == -INFINITY ? 0.f : ex2(old.y - top);
+                        mrow[tid] = make_float2(top + kSlack, top);
+                    }
+                    frow[tid] = f;
+                }
+                named_bar(bar, 128);
+                if (!first) {
+#pragma unroll
+                    for (int c = 0; c < RW; c += 8) {
+                        if (c >= rows) break;
                         float o[8];
-                        tmem_ld8(tO + 32 * hb + c, o);
+                        tmem_ld8(tO + c, o);
                         tmem_wait_ld();
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const float f = frow[32 * hb + c + i];
-                            l[32 * hb + c + i] *= f;
+                            const float f = frow[c + i];
+                            l[c + i] *= f;
                             o[i] *= f;
                         }
-                        tmem_st8(tO + 32 * hb + c, o);
+                        tmem_st8(tO + c, o);
                     }
                     tmem_wait_st();
                 }
-#pragma unroll
-                for (int c = 0; c < WD; c += 8) {
-                    if (32 * hb + c >= mt.rows) break;
-                    uint32_t pk[4];
-#pragma unroll
-                    for (int i = 0; i < 8; i += 2) {
-                        const float4 m = *reinterpret_cast<const float4*>(mrow + 32 * hb + c + i);
-                        const float a = ex2(s[c + i] - m.y), b = ex2(s[c + i + 1] - m.w);
-                        l[32 * hb + c + i] += a;
-                        l[32 * hb + c + i + 1] += b;
-                        pk[i / 2] = F8 ? pack_half2(a, b) : pack_bf16x2(a, b);
-                    }
-                    *reinterpret_cast<uint4*>(sm + C::PM + ((32 * hb + c) / 8) * (TOK * 16) + key * 16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                }
             }
-            if (!F8 && !ok) {   // a value row that was not fetched
+#pragma unroll
+            for (int c = 0; c < RW; c += 8) {
+                if (c >= rows) break;
+                uint32_t pk[4];
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    const float4 m = *reinterpret_cast<const float4*>(mrow + c + i);
+                    const float a = ex2(s[c + i] - m.y), b = ex2(s[c + i + 1] - m.w);
+                    l[c + i] += a;
+                    l[c + i + 1] += b;
+                    pk[i / 2] = F8 ? pack_half2(a, b) : pack_bf16x2(a, b);
+                }
+                *reinterpret_cast<uint4*>(sm + C::PM + ((row0 + c) / 8) * (TOK * 16) + key * 16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            }
+            if (!F8 && !ok && row0 == 0) {   // a value row that was not fetched
                 bad = bad || !wait(full_bar(t), full_phase(t));
                 uint8_t* v = sm + (v_image(t) - sb);
 #pragma unroll
                 for (int x = 0; x < D / 8; ++x)
                     *reinterpret_cast<uint4*>(v + (x >> 3) * C::HALF + sm100::sw128_off(key, x & 7)) = make_uint4(0u, 0u, 0u, 0u);
             }
-            if (edge) {
+            if (edge && mt.nq > 1) {
                 bad = bad || !wait(F8 ? sb + C::VFULL : full_bar(t), F8 ? t & 1 : full_phase(t));
-                sanitize(mt, t, ok, w, lane, pos, neg);
+                sanitize(mt, t, ok, wq, lane, row0, pos, neg);
             }
             tc_fence_before();
             fence_proxy_async_smem();
@@ -543,77 +554,97 @@ struct TcKernel {
                 mbar_arrive(sb + C::SFREE + 8 * (t & 1));
                 mbar_arrive(sb + C::PFULL);
             }
-            if (mt.flags & kLast) {
-                bad = bad || !wait(sb + C::PVDONE + 8 * (t & 1), (t >> 1) & 1);
-                tc_fence_after();
-                epilogue(mt, tO, l, pos, neg, w, lane);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(sb + C::OFREE + 8 * (mt.item & 1));
+            if (!(mt.flags & kLast)) continue;
+
+            // the item's end here: the sums while the last product runs, then the outputs
+            float* to = P.partial + (int64_t)mt.part * (N * (D + 2)) + row0;   // of a split item
+            // sums over the warp's keys: lane i of the first 16 ends with row 16 x + i
+#pragma unroll
+            for (int x = 0; x < RW / 16; ++x) {
+                if (16 * x >= rows) break;
+                float v[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = l[16 * x + i] + __shfl_xor_sync(0xffffffffu, l[16 * x + i], 16);
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+                    for (int i = 0; i < o; ++i) {
+                        const bool hi = lane & o;
+                        const float give = hi ? v[i] : v[i + o], keep = hi ? v[i + o] : v[i];
+                        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                    }
+                if (lane < 16) wred[wq * N + 16 * x + lane] = v[0];
+            }
+            named_bar(bar, 128);
+            float sum = 0.f, top = 0.f;
+            if (tid < rows) {
+                sum = wred[tid] + wred[N + tid] + wred[2 * N + tid] + wred[3 * N + tid];
+                const float2 m = mrow[tid];
+                top = m.x == -INFINITY ? -INFINITY : m.y;
+                const float vs = F8 && P.c.v_scale ? P.c.v_scale[mt.h] : 1.f;
+                frow[tid] = mt.part >= 0 ? 1.f : sum == 0.f ? 0.f : vs / sum;
+            }
+            named_bar(bar, 128);
+            bad = bad || !wait(sb + C::PVDONE + 8 * (t & 1), (t >> 1) & 1);
+            tc_fence_after();
+            const int d = channel(wq, lane);
+            tok = mt.tok0;
+            left = mt.left0;
+            if (row0) {
+                tok = (mt.block * N + row0) / P.group;
+                left = (tok + 1) * P.group - (mt.block * N + row0);
+            }
+            const int64_t at0 = (mt.t0 + tok) * P.Hq + mt.h * P.group + (P.group - left);   // output row
+            if (mt.part < 0) {
+                __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(P.out) + at0 * D + d;
+                const int64_t step = (int64_t)(P.Hq - P.group + 1) * D;   // to the next token's first row
+#pragma unroll
+                for (int c = 0; c < RW; c += 8) {
+                    if (c >= rows) break;
+                    float o[8];
+                    tmem_ld8(tO + c, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float x = o[i];
+                        x += (pos >> (c + i)) & 1 ? INFINITY : 0.f;   // what sanitize has noted
+                        x -= (neg >> (c + i)) & 1 ? INFINITY : 0.f;
+                        if ((c + i < rows) & (d >= 0)) *dst = __float2bfloat16_rn(x * frow[c + i]);
+                        const bool over = --left == 0;
+                        dst += over ? step : D;
+                        left = over ? P.group : left;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < RW; c += 8) {
+                    if (c >= rows) break;
+                    float o[8];
+                    tmem_ld8(tO + c, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float x = o[i];
+                        x += (pos >> (c + i)) & 1 ? INFINITY : 0.f;
+                        x -= (neg >> (c + i)) & 1 ? INFINITY : 0.f;
+                        if ((c + i < rows) & (d >= 0)) to[2 * N + row0 * (D - 1) + (c + i) * D + d] = x;
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sb + C::OFREE + 8 * (mt.item & 1));
+            if (tid < rows) {
+                if (mt.part >= 0) {
+                    to[tid] = top;
+                    to[N + tid] = sum;
+                } else if (P.lse) {
+                    const int ir = mt.block * N + row0 + tid, tk = ir / P.group;
+                    P.lse[(mt.t0 + tk) * P.Hq + mt.h * P.group + (ir - tk * P.group)] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
+                }
             }
         }
         if (bad) fail();
-    }
-
-    __device__ __forceinline__ void epilogue(const Meta& mt, uint32_t tO, float (&l)[N], uint64_t pos, uint64_t neg, int w, int lane) {
-        using namespace sm100;
-        const float2* mrow = reinterpret_cast<const float2*>(sm + C::MROW);
-        float* wred = reinterpret_cast<float*>(sm + C::WRED);
-        float* frow = reinterpret_cast<float*>(sm + C::FROW);
-        const int tid = 32 * w + lane, d = channel(w, lane);
-        float* to = P.partial + (int64_t)mt.part * (N * (D + 2));
-        // sums over the warp's keys: lane i of the first 16 ends with row 16 x + i
-#pragma unroll
-        for (int x = 0; x < N / 16; ++x) {
-            if (16 * x >= mt.rows) break;
-            float v[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = l[16 * x + i] + __shfl_xor_sync(0xffffffffu, l[16 * x + i], 16);
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1)
-#pragma unroll
-                for (int i = 0; i < o; ++i) {
-                    const bool hi = lane & o;
-                    const float give = hi ? v[i] : v[i + o], keep = hi ? v[i + o] : v[i];
-                    v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-                }
-            if (lane < 16) wred[w * N + 16 * x + lane] = v[0];
-        }
-        bar_sync_fixed<1>(128);
-        if (tid < mt.rows) {
-            const float sum = wred[tid] + wred[N + tid] + wred[2 * N + tid] + wred[3 * N + tid];
-            const float2 m = mrow[tid];
-            if (mt.part < 0) {
-                const int ir = mt.block * N + tid, tok = ir / P.group;
-                const float vs = F8 && P.c.v_scale ? P.c.v_scale[mt.h] : 1.f;
-                frow[tid] = sum == 0.f ? 0.f : vs / sum;
-                if (P.lse)
-                    P.lse[(mt.t0 + tok) * P.Hq + mt.h * P.group + (ir - tok * P.group)] = sum == 0.f ? -INFINITY : m.y * kLn2 + logf(sum);
-            } else {
-                to[tid] = m.x == -INFINITY ? -INFINITY : m.y;
-                to[N + tid] = sum;
-            }
-        }
-        bar_sync_fixed<1>(128);
-        int tok = (mt.block * N) / P.group, left = (tok + 1) * P.group - mt.block * N;
-        int64_t at = (mt.t0 + tok) * P.Hq + mt.h * P.group + (P.group - left);   // output row
-#pragma unroll 1
-        for (int c = 0; c < mt.rows; c += 8) {
-            float o[8];
-            tmem_ld8(tO + c, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = c + i;
-                if (r < mt.rows && d >= 0) {
-                    const float x = pos | neg ? poisoned(o[i], r, pos, neg) : o[i];
-                    if (mt.part < 0) static_cast<__nv_bfloat16*>(P.out)[at * D + d] = __float2bfloat16_rn(x * frow[r]);
-                    else to[2 * N + r * D + d] = x;
-                }
-                ++at;
-                if (--left == 0) { at += P.Hq - P.group; left = P.group; }
-            }
-        }
     }
 
     __device__ __forceinline__ void run() {
@@ -643,11 +674,11 @@ struct TcKernel {
             }
             for (int i = 0; i < 2; ++i) {
                 sm100::mbar_init(sb + C::SFULL + 8 * i, 1);
-                sm100::mbar_init(sb + C::SFREE + 8 * i, 4);
+                sm100::mbar_init(sb + C::SFREE + 8 * i, C::SW);
                 sm100::mbar_init(sb + C::PVDONE + 8 * i, 1);
-                sm100::mbar_init(sb + C::OFREE + 8 * i, 4);
+                sm100::mbar_init(sb + C::OFREE + 8 * i, C::SW);
             }
-            sm100::mbar_init(sb + C::PFULL, 4);
+            sm100::mbar_init(sb + C::PFULL, C::SW);
             sm100::mbar_init(sb + C::FIN, 1);
             sm100::fence_mbar_init();
             *reinterpret_cast<volatile uint32_t*>(sm + C::ABORT) = 0;
@@ -656,14 +687,14 @@ struct TcKernel {
         __syncthreads();
         sm100::tc_fence_after();
         const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + C::TMEM);
-        if (warp < 4) {
+        if (warp < C::SW) {
             softmax(tmem, warp, lane);
-        } else if (warp == 4) {
+        } else if (warp == C::SW) {
             fetcher(w, lane);
-        } else if (warp == 5) {
+        } else if (warp == C::SW + 1) {
             issuer(tmem);
         } else {
-            if constexpr (F8) converter(warp - 6, lane);
+            if constexpr (F8) converter(warp - C::SW - 2, lane);
         }
         sm100::tc_fence_before();
         __syncthreads();
