@@ -59,9 +59,6 @@ constexpr int kWorkers = 148;      // one CTA per SM
 constexpr int kGroups = 1024;      // entries of the table of work in shared memory
 constexpr int kMaxSmem = 232448;   // dynamic shared memory of a CTA
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-// The running maximum follows the scores only when they exceed it by 2^8: until then weights are
-// up to 2^8, which fp32 sums, bf16 and fp16 weights hold as well, and acc is not rescaled.
-constexpr float kSlack = 8.f;
 
 // One sequence's share: its new tokens, the keys [lo, hi) that any of them sees, and its tiles.
 struct Seq {
@@ -129,6 +126,16 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
         if (sm100::mbar_try_wait(bar, parity)) return true;
     return false;
 }
+// The same by a whole warp, whose lanes leave it together: what follows (tcgen05.ld, barriers) wants
+// them so.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu, sm100::mbar_try_wait(bar, parity))) return true;
+    const long long t0 = clock64();
+    while (true) {
+        if (__all_sync(0xffffffffu, sm100::mbar_try_wait(bar, parity))) return true;
+        if (__any_sync(0xffffffffu, clock64() - t0 > 2000000000ll)) return false;
+    }
+}
 // TMA box loads; all boxes start at a multiple of 16 bytes of the innermost axis.
 __device__ __forceinline__ void tma4(uint32_t dst, const CUtensorMap* map, int x, int row, int head, int page, uint32_t bar) {
     asm volatile(
@@ -143,13 +150,21 @@ __device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap* map, int x
 // Barrier `id` of `count` threads that tells all of them whether `p` holds for any.
 __device__ __forceinline__ bool bar_any(uint32_t id, bool p, uint32_t count) {
     uint32_t r;
+    __syncwarp();
     asm volatile(
         "{\n\t.reg .pred a, b;\n\t"
         "setp.ne.u32 a, %1, 0;\n\t"
         "barrier.cta.red.or.pred b, %2, %3, a;\n\t"
         "selp.u32 %0, 1, 0, b;\n\t}"
         : "=r"(r) : "r"((uint32_t)p), "r"(id), "r"(count) : "memory");
+    __syncwarp();
     return r != 0;
+}
+
+// Barrier `id` of `count` threads.
+__device__ __forceinline__ void bar_all(uint32_t id, uint32_t count) {
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
+    __syncwarp();
 }
 
 // What the fetching warp tells the other warps of a tile.
@@ -243,19 +258,27 @@ struct Walk {
             s = seq_info<TOK>(P, n, ROWS);
             items = (int64_t)s.blocks * P.c.Hkv;
         }
-        const int64_t a = base + (at - base) / s.tiles * s.tiles, b = a + s.tiles;
-        const int x = (int)((at - base) / s.tiles);
+        const int x = quotient(at - base, s.tiles);
+        const int64_t a = base + (int64_t)x * s.tiles, b = a + s.tiles;
         h = x / s.blocks;
         block = x - h * s.blocks;
+        rows = min(ROWS, s.nq * P.group - block * ROWS);
+        tok0 = block * ROWS / P.group;
+        all_lo = first_key(P, s.start, s.pos0 + s.nq - 1);
         tile = s.tile0 + (int)(at - a);
         tiles = (int)(min(b, end) - at);
         starts = a >= begin;
         ends = b <= end;
-        last_worker = (int)((b - 1) / per);
+        last_worker = quotient(b - 1, per);
         i = 0;
         ++item;
     }
-    int last_worker;
+    int last_worker, rows, tok0, all_lo;
+
+    // a / b < 2^31; 64-bit division takes four times as long as 32-bit
+    static __device__ __forceinline__ int quotient(int64_t a, int64_t b) {
+        return ((a | b) >> 32) == 0 ? (int)((uint32_t)a / (uint32_t)b) : (int)(a / b);
+    }
 
     __device__ __forceinline__ int j0() const { return (tile + i) * TOK; }
     __device__ __forceinline__ void next() {
@@ -263,21 +286,21 @@ struct Walk {
         if (++i == tiles && at < end) seek();
     }
     __device__ __forceinline__ void fill(Meta* m) const {
-        const int j = j0(), all_lo = first_key(P, s.start, s.pos0 + s.nq - 1);
+        const int j = j0();
         const bool inside = j >= all_lo && j + TOK - 1 <= min(s.pos0, s.hi - 1);
         m->t0 = s.t0;
         m->j0 = j;
         m->flags = (i == 0 ? kFirst : 0) | (i == tiles - 1 ? kLast : 0) | (inside ? 0 : kEdge);
         m->h = h;
         m->block = block;
-        m->rows = min(ROWS, s.nq * P.group - block * ROWS);
+        m->rows = rows;
         m->nq = s.nq;
         m->pos0 = s.pos0;
         m->start = s.start;
         m->all_lo = all_lo;
         m->item = item;
-        m->tok0 = block * ROWS / P.group;
-        m->left0 = (m->tok0 + 1) * P.group - block * ROWS;
+        m->tok0 = tok0;
+        m->left0 = (tok0 + 1) * P.group - block * ROWS;
         m->part = starts && ends ? -1 : 2 * (int)blockIdx.x + (starts ? 1 : 0);
     }
     __device__ __forceinline__ void tell_join(Split* to) const {
@@ -286,7 +309,7 @@ struct Walk {
 };
 
 // The fetching warp.  C: the kernel's layout: TOK keys a tile; operands in blocks of BLK channels,
-// each a run of 128-byte rows (e4m3: the whole row), RAW bytes apart for keys and values.
+// each a run of rows of BROWB bytes; values lie RAW bytes behind the keys.
 template <typename C, int ROWS>
 struct Fetch {
     static constexpr int RPL = C::TOK / 32;   // rows of a lane
@@ -311,7 +334,9 @@ struct Fetch {
     }
     // Fetches the tile that the walk stands at (and, with an item's first, its queries at q) and
     // fills in what the others need to know of it.
-    __device__ __forceinline__ void put(const W& w, uint32_t stage, uint32_t q, uint32_t bar, uint32_t meta_bar, Meta* meta, uint32_t* okm) {
+    // Queries with a barrier of their own come with *last: whether it is the stretch's last item.
+    __device__ __forceinline__ void put(const W& w, uint32_t stage, uint32_t q, uint32_t bar, uint32_t qbar, uint32_t meta_bar, Meta* meta,
+                                        uint32_t* okm, uint32_t* last) {
         const int j0 = w.j0(), box = 1 << P.box_shift;
         uint32_t bits = 0, boxes = 0;
         bool wrong = false;
@@ -334,18 +359,20 @@ struct Fetch {
         __syncwarp();
         if (lane == 0) {
             sm100::mbar_arrive(meta_bar);
-            sm100::mbar_arrive_expect_tx(bar, boxes * (uint32_t)(2 * box * C::ROWB) + (w.i == 0 ? C::QB : 0));
+            const uint32_t queries = w.i == 0 ? C::QB : 0;
+            sm100::mbar_arrive_expect_tx(bar, boxes * (uint32_t)(2 * box * C::ROWB) + (qbar == bar ? queries : 0));
+            if (qbar != bar && queries) *last = w.at + w.tiles >= w.end;
+            if (qbar != bar && queries) sm100::mbar_arrive_expect_tx(qbar, queries);
         }
         __syncwarp();
         if (w.i == 0) {
-            const int rows = w.s.nq * P.group - w.block * ROWS;
             for (int r = lane; r < ROWS; r += 32) {
                 const int ir = w.block * ROWS + r, tok = ir / P.group, g = ir - tok * P.group;
                 // rows behind the item's: a token behind the last one, which TMA fills with zeros
-                const int head = r < rows ? w.h * P.group + g : 0, token = r < rows ? (int)w.s.t0 + tok : (int)P.total;
+                const int head = r < w.rows ? w.h * P.group + g : 0, token = r < w.rows ? (int)w.s.t0 + tok : (int)P.total;
 #pragma unroll
                 for (int b = 0; b < C::QBLKS; ++b)
-                    tma3(q + b * C::QBLOCK + r * C::QROWB, &P.q_map, b * (C::D / C::QBLKS), head, token, bar);
+                    tma3(q + b * C::QBLOCK + r * C::QROWB, &P.q_map, b * (C::D / C::QBLKS), head, token, qbar);
             }
         }
 #pragma unroll
@@ -353,7 +380,7 @@ struct Fetch {
             const int r = lane * RPL + x;
             if (page[x] < 0 || (r & (box - 1)) != 0) continue;
             const int row = (j0 + r) & ((1 << P.c.page_shift) - 1);
-            const uint32_t dst = stage + r * C::pitch(P.box_shift);
+            const uint32_t dst = stage + r * C::BROWB;
 #pragma unroll
             for (int b = 0; b < C::BLKS; ++b) {
                 tma4(dst + b * C::BLOCK, &P.k_map, b * (C::D / C::BLKS), row, w.h, page[x], bar);
@@ -382,6 +409,10 @@ struct Fetch {
         return true;
     }
 };
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 
 // Adds up the partial triples of the items that lie across stretches.  CTA (w, row): the item
 // that starts in worker w's stretch and goes on; groups of D threads share its parts.
@@ -475,7 +506,8 @@ bool make_maps(Params& P, int64_t D, int esz, CUtensorMapDataType type, CUtensor
     const cuuint64_t strides[3] = {dims[1] > 1 ? (cuuint64_t)P.c.row_stride * esz : one, dims[2] > 1 ? (cuuint64_t)P.c.head_stride * esz : one,
                                    dims[3] > 1 ? (cuuint64_t)P.c.page_stride * esz : one};
     const cuuint32_t boxes[4] = {(cuuint32_t)(D / C::BLKS), 1u << box, 1, 1}, ones[4] = {1, 1, 1, 1};
-    const CUtensorMapSwizzle swizzle = C::SWIZZLED ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE;
+    const CUtensorMapSwizzle swizzle = C::BROWB == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+    if (C::BROWB << box < 128) return false;   // a box lands at a multiple of 128 bytes
     for (int x = 0; x < 2; ++x)
         // without pages nothing is read
         if (encode(x ? &P.v_map : &P.k_map, type, 4, P.c.num_pages == 0 ? const_cast<void*>(P.q) : x ? P.c.v : P.c.k, dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,

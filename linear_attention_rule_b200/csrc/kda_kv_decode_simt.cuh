@@ -18,9 +18,8 @@ struct Simt {
     static constexpr int TOK = 32 * 128 / D, CW = 8, THREADS = 32 * (CW + 1);
     static constexpr int ROWB = 4 * D, RAW = TOK * ROWB, STAGE = 2 * RAW;
     // for Fetch: blocks of 32 channels, 128-byte rows
-    static constexpr bool SWIZZLED = true, QSWIZZLED = false;
-    static constexpr int BLKS = D / 32, BLOCK = TOK * 128, QBLKS = 1, QROWB = ROWB, QBLOCK = 0;
-    static __host__ __device__ constexpr int pitch(int) { return 128; }
+    static constexpr bool QSWIZZLED = false;
+    static constexpr int BLKS = D / 32, BROWB = 128, BLOCK = TOK * 128, QBLKS = 1, QROWB = ROWB, QBLOCK = 0;
     static constexpr int STG = 6, QS = STG, MD = STG + 2;
     static constexpr int PARTS = 32 * CW / TOK, KPW = 32 / PARTS;    // lanes of a key, keys of a warp
     static constexpr int GROUPS = 32 * CW / D;                       // threads of a channel, 16 keys each
@@ -54,11 +53,11 @@ struct SimtKernel {
         const bool ok = f.run(
             w, T,
             [&](int t) {
-                return !aborted() && (t < C::STG || wait(sb + C::EMPTY + 8 * (t % C::STG), (t / C::STG - 1) & 1));
+                return !aborted() && (t < C::STG || wait_warp(sb + C::EMPTY + 8 * (t % C::STG), (t / C::STG - 1) & 1));
             },
             [&](int t) {
                 f.put(w, sb + (t % C::STG) * C::STAGE, sb + C::Q + (w.item % C::QS) * C::QB, sb + C::FULL + 8 * (t % C::STG),
-                      sb + C::MFULL + 8 * (t % C::MD), meta(t), reinterpret_cast<uint32_t*>(sm + C::OKM + (t % C::MD) * 16));
+                      sb + C::FULL + 8 * (t % C::STG), sb + C::MFULL + 8 * (t % C::MD), meta(t), reinterpret_cast<uint32_t*>(sm + C::OKM + (t % C::MD) * 16), nullptr);
             });
         if (!ok) fail();
         // copies still in flight at the end of an aborted run
@@ -79,7 +78,7 @@ struct SimtKernel {
         float acc[R], m = -INFINITY, l = 0.f;   // m, l: of row w
         bool bad = false;
         for (int t = 0; t < T; ++t) {
-            bad = bad || !wait(sb + C::FULL + 8 * (t % C::STG), (t / C::STG) & 1);
+            bad |= !wait_warp(sb + C::FULL + 8 * (t % C::STG), (t / C::STG) & 1);
             if (bar_any(1, bad || aborted(), NT)) break;
             const Meta mt = *meta(t);
             const uint32_t* okm = reinterpret_cast<const uint32_t*>(sm + C::OKM + (t % C::MD) * 16);
@@ -127,7 +126,7 @@ struct SimtKernel {
                     }
                 }
             }
-            sm100::bar_sync_fixed<1>(NT);
+            bar_all(1, NT);
             if (w < mt.rows) {
                 float x[TOK / 32], top = -INFINITY;
 #pragma unroll
@@ -147,7 +146,7 @@ struct SimtKernel {
                 }
                 if (lane == 0) frow[w] = f;
             }
-            sm100::bar_sync_fixed<1>(NT);
+            bar_all(1, NT);
             {
                 float vv[16];
 #pragma unroll
@@ -186,7 +185,7 @@ struct SimtKernel {
 #pragma unroll
                         for (int r = 0; r < R; ++r) red[r * D + d] = g == 0 ? acc[r] : red[r * D + d] + acc[r];
                     }
-                    sm100::bar_sync_fixed<1>(NT);
+                    bar_all(1, NT);
                 }
                 float* to = P.partial + (int64_t)mt.part * (R * (D + 2));
                 for (int x = tid; x < mt.rows * D; x += NT) {
@@ -210,6 +209,7 @@ struct SimtKernel {
 
     __device__ __forceinline__ void run() {
         const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+        if (tid == 0) { prefetch_map(&P.k_map); prefetch_map(&P.v_map); prefetch_map(&P.q_map); }
         W w(P);
         w.template find<C::THREADS>(reinterpret_cast<int64_t*>(sm));
         kda_grid_launch_next();

@@ -11,15 +11,19 @@
 //
 // Warps: 4 for softmax and epilogue (TMEM lanes 32 w ..) for every 16 rows (8 with 32 and 64), which
 // share nothing but keys and values; then one that fetches tiles, one that issues the products, and
-// with an e4m3 cache those that convert.  S and O are double-buffered in TMEM, so the product of the next tile
-// runs during the softmax of this one and the next item starts during the epilogue of the last.
+// with an e4m3 cache four that split queries.  S and O are double-buffered in TMEM, so the product
+// of the next tile runs during the softmax of this one and the next item starts during the epilogue
+// of the last.  Tiles land in the operand images directly: TMA's swizzle is the images'.
 //
-// bf16: tiles land in the operand images directly (TMA's 128-byte swizzle is the images').
-// e4m3: tcgen05 has no product of 8-bit with 16-bit operands, and queries or weights in 8 bits
-// would lose what the scores need.  e4m3 is exact in fp16, so raw rows land in a ring of their own
-// and are turned into fp16 images (K and V one buffer each).  Weights then are fp16 (2^-11), and
-// a query row is scaled by a power of two to a largest element in [1, 2): bf16 has 8 bits, fp16
-// keeps them all down to 2^-14 of the row's largest, and below that 2^-25 of it.
+// e4m3: tcgen05 multiplies 8-bit with 8-bit operands only, and queries or weights rounded to 8 bits
+// would lose what the scores need.  So they are split into e4m3 parts that sum up to them, side by
+// side in N, which costs nothing while the long operand bounds the product:
+//   a query row is scaled by a power of two to a largest element in [2^7, 2^8); q = q1 + q2 / 16
+//     holds bf16's 8 bits, down to 2^-22 of the row's largest;
+//   a weight, in fp16 (2^-11), is p1 + p2 / 16 + p3 / 256 exactly, down to 2^-26 of the row's largest.
+// The products are exact and summed in fp32: 2^-25 of the sum of magnitudes over 128 products.  The
+// other way, turning the cache's tiles into fp16 images, took eight warps 1,900 cycles an operand and
+// four times the shared-memory traffic: 151 us for 75,800 keys of 8 heads.
 #pragma once
 
 #include "kda_kv_decode.cuh"
@@ -34,52 +38,68 @@ struct Tc {
     static constexpr bool F8 = sizeof(TC) == 1;
     static constexpr int TOK = 128;
     static constexpr int SW = N >= 32 ? 8 : 4, RW = N / (SW / 4);             // softmax warps, rows of four of them
-    static constexpr int LW = F8 ? (N >= 32 ? 4 : 8) : 0, RPW = F8 ? TOK / LW : TOK;   // converting warps, keys of each
+    static constexpr int LW = F8 ? 4 : 0;                                     // splitting warps
     static constexpr int THREADS = 32 * (SW + 2 + LW);
-    static constexpr int ROWB = D * (int)sizeof(TC), CPR = ROWB / 16;  // a cache row
-    static constexpr int OP = TOK * D * 2;                             // an operand image: D / 64 halves of 128-byte rows
-    static constexpr int HALF = TOK * 128, QHALF = N * 128;
-    static constexpr int RAW = TOK * 128 * (F8 || D == 64 ? 1 : 2);
-    // for Fetch
-    static constexpr bool SWIZZLED = !F8, QSWIZZLED = true;
-    static constexpr int BLKS = F8 ? 1 : D / 64, BLOCK = HALF;
-    // from row to row; a box starts at a multiple of 128 bytes, boxes of one 64-byte row too
-    static __host__ __device__ constexpr int pitch(int box_shift) { return F8 && box_shift > 0 ? ROWB : 128; }
-    static constexpr int QBLKS = D / 64, QROWB = 128, QBLOCK = QHALF;
-    static constexpr int QB = N * D * 2, PB = N * TOK * 2;
-    static constexpr int FIXED = F8 ? 2 * OP : 0;                      // the fp16 images
+    static constexpr int QP = F8 ? 2 : 1, PP = F8 ? 3 : 1;                    // parts of queries and weights
+    // The running maximum follows the scores only when they exceed it by SLACK (in units of log 2):
+    // until then acc is not rescaled.  Weights are 2^(s - m + BASE): up to 2^8, which fp32 sums and bf16
+    // weights hold as well as 1; with e4m3 parts from 2^8 (the smallest parts then lie furthest below
+    // the largest weight) to 430 (e4m3 ends at 448).
+    static constexpr float BASE = F8 ? 8.f : 0.f, SLACK = F8 ? 0.75f : 8.f;
+    static constexpr int ROWB = D * (int)sizeof(TC);                   // a cache row
+    // an operand image: BLKS blocks of rows of BROWB bytes, swizzled over those
+    static constexpr int BROWB = ROWB < 128 ? ROWB : 128, BLKS = ROWB / BROWB, BLOCK = TOK * BROWB, RAW = TOK * ROWB;
+    static constexpr int KSTEP = F8 ? 32 : 16;                         // of one tcgen05.mma
+    static constexpr uint32_t SWZ = BROWB == 64 ? sm100::kSwizzle64 : sm100::kSwizzle128;
     static constexpr int STAGE = 2 * RAW;
-    // Slots are reused once a tile before them is known to be done.  A stage is free when its tile t
-    // is done (bf16), or converted, and then tile t - 1 is done (e4m3): queries need one slot per
-    // stage, e4m3 one more; meta is read a little longer.
-    static constexpr int qslots(int stg) { return stg + (F8 ? 1 : 0); }
+    // queries: D bf16 in blocks of 128-byte rows; split, QP N rows of the cache's form in the same place
+    static constexpr bool QSWIZZLED = true;
+    static constexpr int QBLKS = D / 64, QROWB = 128, QBLOCK = N * 128, QB = N * D * 2;
+    static constexpr int PG = 16 / (F8 ? 1 : 2);                       // rows of a 16-byte chunk of weights
+    static constexpr int PB = PP * N * TOK * (F8 ? 1 : 2);
+    static constexpr int OB = 2 * (QP + PP) * N <= 512 ? 2 : 1;        // O buffers that Tensor Memory has room for
+    static constexpr int COLS = (2 * QP + OB * PP) * N;
+    static constexpr int TCOLS = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+    // A stage is free when its tile is done; queries need one slot per stage, meta is read a little longer.
     static constexpr int metas(int stg) { return stg + 2; }
     static constexpr int misc(int stg) {
-        return metas(stg) * 64 + metas(stg) * 16 + qslots(stg) * N * 4 + N * 8 + N * 8 + 4 * N * 4 + N * 4 + 8 * (2 * stg + metas(stg) + 18) + 32;
+        return metas(stg) * 64 + metas(stg) * 16 + stg * N * 4 + N * 8 + N * 8 + 4 * N * 4 + N * 4 + 8 * (4 * stg + metas(stg) + 12) + 32 + stg * 4;
     }
-    static constexpr int total(int stg) { return FIXED + stg * STAGE + qslots(stg) * QB + PB + misc(stg); }
+    static constexpr int total(int stg) { return stg * (STAGE + QB) + PB + misc(stg); }
     static constexpr int most(int stg) { return stg > 2 && total(stg) > kMaxSmem ? most(stg - 1) : stg; }
-    static constexpr int STG = most(6), QS = qslots(STG), MD = metas(STG);
+    static constexpr int STG = most(6), QS = STG, MD = metas(STG);
     static constexpr int BYTES = total(STG);
     static_assert(BYTES <= kMaxSmem, "shared memory of a CTA");
     static_assert((kGroups + 1) * 8 + 32 * 8 <= STG * STAGE, "the table of work lies where the ring comes");
     // offsets
-    static constexpr int RING = FIXED, Q = RING + STG * STAGE, PM = Q + QS * QB, META = PM + PB, OKM = META + MD * 64,
+    static constexpr int RING = 0, Q = RING + STG * STAGE, PM = Q + QS * QB, META = PM + PB, OKM = META + MD * 64,
                          QF = OKM + MD * 16, RINFO = QF + QS * N * 4, MROW = RINFO + N * 8, WRED = MROW + N * 8,
                          FROW = WRED + 4 * N * 4, BAR = FROW + N * 4;
     static_assert(META % 16 == 0 && OKM % 16 == 0 && RINFO % 16 == 0 && BAR % 8 == 0, "alignment");
     // barriers
-    static constexpr int FULL = BAR, EMPTY = FULL + 8 * STG, MFULL = EMPTY + 8 * STG, KFULL = MFULL + 8 * MD, KFREE = KFULL + 8,
-                         VFULL = KFREE + 8, VFREE = VFULL + 8, QFULL = VFREE + 8, SFULL = QFULL + 16, SFREE = SFULL + 16,
-                         PFULL = SFREE + 16, PVDONE = PFULL + 8, OFREE = PVDONE + 16, FIN = OFREE + 16, TMEM = FIN + 8, ABORT = TMEM + 4, BITS = ABORT + 4;
-    static_assert(BITS + 16 <= BYTES, "misc");
-    static constexpr int TCOLS = 4 * N;   // S twice, O twice
+    static constexpr int FULL = BAR, EMPTY = FULL + 8 * STG, QRAW = EMPTY + 8 * STG, QFULL = QRAW + 8 * QS, MFULL = QFULL + 8 * QS,
+                         SFULL = MFULL + 8 * MD, SFREE = SFULL + 16, PFULL = SFREE + 16, PVDONE = PFULL + 8, OFREE = PVDONE + 16,
+                         FIN = OFREE + 16, TMEM = FIN + 8, ABORT = TMEM + 4, BITS = ABORT + 4, QLAST = BITS + 16;
+    static_assert(QLAST + QS * 4 <= BYTES, "misc");
+    // byte offset of 16-byte chunk ch of a row of an image
+    static __device__ __forceinline__ uint32_t chunk(uint32_t row, uint32_t ch) {
+        return BROWB == 64 ? sm100::sw64_off(row, ch) : (ch >> 3) * BLOCK + sm100::sw128_off(row, ch & 7);
+    }
 };
 
-__host__ __device__ constexpr uint32_t idesc16(bool bf16, int M, int N, bool a_mn, bool b_mn) {
+// Instruction descriptor: bf16 (kind::f16) or e4m3 (kind::f8f6f4) operands, fp32 accumulate.
+__host__ __device__ constexpr uint32_t idesc(bool bf16, int M, int N, bool a_mn, bool b_mn) {
     const uint32_t f = bf16 ? 1u : 0u;
     return (1u << 4) | (f << 7) | (f << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a), "l"(b), "r"(id), "r"(accumulate)
+        : "memory");
 }
 
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
@@ -112,15 +132,9 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
                  ::"r"(taddr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
                  : "memory");
 }
-__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t lo16) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)lo16, __NV_E4M3);
-    return (uint32_t)h.x | ((uint32_t)h.y << 16);
-}
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) { return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3); }
+__device__ __forceinline__ uint32_t e4m3x2(__half2 x) { return __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3); }
+__device__ __forceinline__ __half2 half2_of(uint32_t e4m3x2) { return __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)e4m3x2, __NV_E4M3)); }
 template <int D, typename TC, int N>
 struct TcKernel {
     typedef Tc<D, TC, N> C;
@@ -146,11 +160,12 @@ struct TcKernel {
         const bool ok = f.run(
             w, T,
             [&](int t) {
-                return !aborted() && (t < C::STG || wait(sb + C::EMPTY + 8 * (t % C::STG), (t / C::STG - 1) & 1));
+                return !aborted() && (t < C::STG || wait_warp(sb + C::EMPTY + 8 * (t % C::STG), (t / C::STG - 1) & 1));
             },
             [&](int t) {
                 f.put(w, sb + C::RING + (t % C::STG) * C::STAGE, sb + C::Q + (w.item % C::QS) * C::QB, sb + C::FULL + 8 * (t % C::STG),
-                      sb + C::MFULL + 8 * (t % C::MD), meta(t), reinterpret_cast<uint32_t*>(sm + C::OKM + (t % C::MD) * 16));
+                      F8 ? sb + C::QRAW + 8 * (w.item % C::QS) : sb + C::FULL + 8 * (t % C::STG), sb + C::MFULL + 8 * (t % C::MD), meta(t), reinterpret_cast<uint32_t*>(sm + C::OKM + (t % C::MD) * 16),
+                      reinterpret_cast<uint32_t*>(sm + C::QLAST) + w.item % C::QS);
             });
         if (!ok) fail();
     }
@@ -159,157 +174,134 @@ struct TcKernel {
         for (int t = max(T - C::STG, 0); t < T; ++t) wait(sb + C::FULL + 8 * (t % C::STG), (t / C::STG) & 1);
     }
 
-    // ------------------------------------------------------------------ e4m3 -> fp16
-    // All of this warp's writes are visible to the tensor core; one arrival per warp.
-    __device__ __forceinline__ void announce(uint32_t bar, int lane) {
-        sm100::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) sm100::mbar_arrive(bar);
-    }
-    // The item's bf16 query rows, in place; the factor that undoes their scaling in qf.
-    __device__ __forceinline__ void convert_queries(int slot, int lw, int lane) {
-        constexpr int E = D / 32;   // channels of a lane
-        const int byte = lane * E * 2;
-#pragma unroll 2
-        for (int r = lw; r < N; r += C::LW) {
-            uint8_t* at = sm + C::Q + slot * C::QB + (byte >> 7) * C::QHALF + sm100::sw128_off(r, (byte & 127) >> 4) + (byte & 15);
-            uint32_t raw[E / 2];
-            if constexpr (E == 4) {
-                const uint2 u = *reinterpret_cast<const uint2*>(at);
-                raw[0] = u.x;
-                raw[1] = u.y;
-            } else {
-                raw[0] = *reinterpret_cast<const uint32_t*>(at);
-            }
-            float top = 0.f;
-#pragma unroll
-            for (int e = 0; e < E / 2; ++e)
-                top = fmaxf(top, fmaxf(fabsf(__uint_as_float(raw[e] << 16)), fabsf(__uint_as_float(raw[e] & 0xffff0000u))));
-            top = warp_max(top);
-            const int ex = (int)((__float_as_uint(top) >> 23) & 255u);
-            const int sh = ex == 0 || ex == 255 ? 0 : ex - 127;   // zeros, and infinities, stay as they are
-            const float down = scalbnf(1.f, -sh);
-#pragma unroll
-            for (int e = 0; e < E / 2; ++e)
-                raw[e] = pack_half2(__uint_as_float(raw[e] << 16) * down, __uint_as_float(raw[e] & 0xffff0000u) * down);
-            if constexpr (E == 4) *reinterpret_cast<uint2*>(at) = make_uint2(raw[0], raw[1]);
-            else *reinterpret_cast<uint32_t*>(at) = raw[0];
-            if (lane == 0) reinterpret_cast<float*>(sm + C::QF)[slot * N + r] = scalbnf(1.f, sh);
-        }
-    }
-    // raw rows of one operand -> its fp16 image; zeros for rows that no token sees
-    __device__ __forceinline__ void convert(uint32_t raw, uint32_t image, uint32_t ok, int lw, int lane) {
-        constexpr int RPI = 32 / C::CPR, ITER = C::RPW / RPI;
-        const int ch = lane % C::CPR, pitch = C::pitch(P.box_shift);
-        uint4 u[ITER];
-#pragma unroll
-        for (int it = 0; it < ITER; ++it)
-            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u[it].x), "=r"(u[it].y), "=r"(u[it].z), "=r"(u[it].w)
-                         : "r"(raw + (lw * C::RPW + it * RPI + lane / C::CPR) * pitch + ch * 16) : "memory");
+    // ------------------------------------------------------------------ queries in two e4m3 parts
+    // bf16 rows of an item -> QP N rows of e4m3, in the same place: everything is read before anything
+    // is written.  What undoes the scaling goes to qf.
+    __device__ __forceinline__ void split_queries(int slot, int lw, int lane) {
+        constexpr int LANES = D / 4, RPI = 32 / LANES;          // lanes of a row, rows of a warp at a time
+        constexpr int ITER = N / (C::LW * RPI);
+        uint8_t* q = sm + C::Q + slot * C::QB;
+        const int sub = lane % LANES, byte = sub * 8;
+        uint32_t one[ITER], two[ITER];
 #pragma unroll
         for (int it = 0; it < ITER; ++it) {
-            const int rl = it * RPI + lane / C::CPR, row = lw * C::RPW + rl;
-            const uint32_t keep = (ok >> rl) & 1 ? 0xffffffffu : 0u;
-            const uint32_t a[4] = {u[it].x & keep, u[it].y & keep, u[it].z & keep, u[it].w & keep};
-            uint32_t h[8];
+            const int r = (it * C::LW + lw) * RPI + lane / LANES;
+            const uint2 u = *reinterpret_cast<const uint2*>(q + (byte >> 7) * C::QBLOCK + sm100::sw128_off(r, (byte & 127) >> 4) + (byte & 15));
+            float x[4] = {__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                          __uint_as_float(u.y & 0xffff0000u)};
+            float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                h[2 * x] = e4m3x2_to_half2(a[x] & 0xffffu);
-                h[2 * x + 1] = e4m3x2_to_half2(a[x] >> 16);
+            for (int o = LANES / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const int ex = (int)((__float_as_uint(top) >> 23) & 255u);
+            const int sh = ex == 0 || ex == 255 ? 0 : ex - 127 - 7;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = ex == 255 ? x[e] - x[e] : scalbnf(x[e], -sh);   // a row with an infinity scores NaN
+            uint32_t a = 0, b = 0;
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                const uint32_t hi = e4m3x2(x[e], x[e + 1]);
+                const float2 h = __half22float2(half2_of(hi));
+                a |= hi << (8 * e);
+                b |= e4m3x2((x[e] - h.x) * 16.f, (x[e + 1] - h.y) * 16.f) << (8 * e);
             }
-            // 16 channels are two chunks; lanes of the two halves of a 128-channel row write them in
-            // opposite order, so that eight lanes cover all banks
-            const uint32_t base = image + (ch >> 2) * C::HALF;
-            const bool swap = (ch >> 2) & 1;
-            const uint32_t c0 = 2 * (ch & 3);
+            one[it] = a;
+            two[it] = b;
+            if (sub == 0) reinterpret_cast<float*>(sm + C::QF)[slot * N + r] = scalbnf(1.f, sh);
+        }
+        bar_all(4, 32 * C::LW);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const bool second = (x == 1) != swap;
-                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(base + sm100::sw128_off(row, c0 + (second ? 1 : 0))),
-                             "r"(second ? h[4] : h[0]), "r"(second ? h[5] : h[1]), "r"(second ? h[6] : h[2]), "r"(second ? h[7] : h[3])
-                             : "memory");
+        for (int it = 0; it < ITER; ++it) {
+            const int r = (it * C::LW + lw) * RPI + lane / LANES;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const uint32_t row = y * N + r;
+                const uint32_t at = (C::BROWB == 64 ? sm100::sw64_off(row, sub >> 2) : sm100::sw128_off(row, sub >> 2)) + (sub & 3) * 4;
+                *reinterpret_cast<uint32_t*>(q + at) = y ? two[it] : one[it];
             }
         }
     }
-    __device__ __forceinline__ void converter(int lw, int lane) {
+    __device__ __forceinline__ void splitter(int lw, int lane) {
         bool ok = true;
-        for (int t = 0; t < T; ++t) {
-            ok = !aborted() && wait(sb + C::FULL + 8 * (t % C::STG), (t / C::STG) & 1);
-            if (!ok) break;
-            const uint32_t raw = sb + C::RING + (t % C::STG) * C::STAGE;
-            const uint32_t seen = reinterpret_cast<const uint32_t*>(sm + C::OKM + (t % C::MD) * 16)[lw * C::RPW / 32] >> (lw * C::RPW % 32);
-            const int item = meta(t)->item;
-            if (meta(t)->flags & kFirst) {
-                convert_queries(item % C::QS, lw, lane);
-                __syncwarp();
-                if (lane == 0) sm100::mbar_arrive(sb + C::QFULL + 8 * (item & 1));
-            }
-            if (t > 0 && !wait(sb + C::KFREE, (t - 1) & 1)) { ok = false; break; }
-            convert(raw, sb, seen, lw, lane);
-            announce(sb + C::KFULL, lane);
-            if (t > 0 && !wait(sb + C::VFREE, (t - 1) & 1)) { ok = false; break; }
-            convert(raw + C::RAW, sb + C::OP, seen, lw, lane);
-            announce(sb + C::VFULL, lane);
-            if (lane == 0) sm100::mbar_arrive(sb + C::EMPTY + 8 * (t % C::STG));
+        for (int item = 0;; ++item) {
+            const int slot = item % C::QS;
+            ok = wait_warp(sb + C::QRAW + 8 * slot, (item / C::QS) & 1);
+            if (bar_any(4, !ok || aborted(), 32 * C::LW)) break;
+            const bool last = reinterpret_cast<const uint32_t*>(sm + C::QLAST)[slot];
+            split_queries(slot, lw, lane);
+            sm100::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) sm100::mbar_arrive(sb + C::QFULL + 8 * slot);
+            if (last) break;
         }
         if (!ok) fail();
     }
 
     // ------------------------------------------------------------------ products
-    __device__ __forceinline__ uint32_t k_image(int t) const { return F8 ? sb : sb + C::RING + (t % C::STG) * C::STAGE; }
-    __device__ __forceinline__ uint32_t v_image(int t) const { return F8 ? sb + C::OP : k_image(t) + C::RAW; }
-    __device__ __forceinline__ uint32_t full_bar(int t) const { return F8 ? sb + C::KFULL : sb + C::FULL + 8 * (t % C::STG); }
-    static __device__ __forceinline__ uint32_t full_phase(int t) { return F8 ? t & 1 : (t / C::STG) & 1; }
+    __device__ __forceinline__ uint8_t* v_image(int t) const { return sm + C::RING + (t % C::STG) * C::STAGE + C::RAW; }
+    __device__ __forceinline__ bool wait_full(int t) const { return wait(sb + C::FULL + 8 * (t % C::STG), (t / C::STG) & 1); }
+    static __device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+        if constexpr (F8) umma_f8(d, a, b, id, accumulate);
+        else sm100::umma_bf16(d, a, b, id, accumulate);
+    }
 
     // Scores of tile s, values of tile p, in whatever order the operands come.  The whole warp walks
     // through (its decisions are votes, so that descriptors stay in uniform registers), one lane issues.
     __device__ __forceinline__ void issuer(uint32_t tmem) {
         using namespace sm100;
-        constexpr uint32_t id_s = idesc16(!F8, 128, N, false, false), id_o = idesc16(!F8, D, N, true, true);
-        const uint64_t k0 = smem_desc(sb + (F8 ? 0 : C::RING), 16, 1024, kSwizzle128), q0 = smem_desc(sb + C::Q, 16, 1024, kSwizzle128);
-        const uint64_t v0 = smem_desc(sb + (F8 ? C::OP : C::RING + C::RAW), C::HALF, 1024, kSwizzle128);
+        constexpr uint32_t id_s = idesc(!F8, 128, C::QP * N, false, false), id_o = idesc(!F8, D, C::PP * N, true, true);
+        constexpr uint32_t SBO = 8 * C::BROWB;
+        // queries, split or not, are rows of BROWB bytes as the keys are
+        const uint64_t k0 = smem_desc(sb + C::RING, 16, SBO, C::SWZ), q0 = smem_desc(sb + C::Q, 16, SBO, C::SWZ);
+        const uint64_t v0 = smem_desc(sb + C::RING + C::RAW, C::BLOCK, SBO, C::SWZ);
         const uint64_t p0 = smem_desc(sb + C::PM, 128, TOK * 16, 0);
-        int s = 0, p = 0, ss = 0, ps = 0;   // tiles, and their stages
-        uint32_t sp = 0;                    // phase of tile s's stage
-        int qslot = -1, item = -1;          // of tile s, of tile p
+        constexpr int KPB = C::BROWB / 32;   // products along a block of channels, 32 bytes each
+        int s = 0, p = 0, ss = 0, ps = 0;    // tiles, and their stages
+        uint32_t sp = 0;                     // phase of tile s's stage
+        int qitem = -1, qslot = -1, item = -1;   // of tile s, of tile p
         long long t0 = 0;
         bool ok = true;
         for (uint32_t idle = 0; p < T;) {
-            bool go = s < T && s < p + 2 && mbar_test(F8 ? sb + C::KFULL : sb + C::FULL + 8 * ss, F8 ? s & 1 : sp) &&
+            bool go = s < T && s < p + 2 && mbar_test(sb + C::FULL + 8 * ss, sp) &&
                       (s < 2 || mbar_test(sb + C::SFREE + 8 * (s & 1), ((s >> 1) - 1) & 1));
             if (__all_sync(0xffffffffu, go)) {
-                tc_fence_after();
-                if (__any_sync(0xffffffffu, meta(s)->flags & kFirst)) qslot = qslot + 1 == C::QS ? 0 : qslot + 1;
-                const uint64_t k = k0 + (F8 ? 0 : (uint32_t)(ss * C::STAGE) >> 4), q = q0 + ((uint32_t)(qslot * C::QB) >> 4);
-                if (elect_one()) {
+                const bool first = __any_sync(0xffffffffu, meta(s)->flags & kFirst);
+                const int it = qitem + (first ? 1 : 0), slot = !first ? qslot : qslot + 1 == C::QS ? 0 : qslot + 1;
+                go = !F8 || !first || mbar_test(sb + C::QFULL + 8 * slot, (it / C::QS) & 1);
+                if (__all_sync(0xffffffffu, go)) {
+                    qitem = it;
+                    qslot = slot;
+                    tc_fence_after();
+                    const uint64_t k = k0 + ((uint32_t)(ss * C::STAGE) >> 4), q = q0 + ((uint32_t)(qslot * C::QB) >> 4);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int x = 0; x < D / 16; ++x)
-                        umma_bf16(tmem + N * (s & 1), k + (((x >> 2) * C::HALF + (x & 3) * 32) >> 4),
-                                  q + (((x >> 2) * C::QHALF + (x & 3) * 32) >> 4), id_s, x > 0);
-                    umma_commit(sb + C::SFULL + 8 * (s & 1));
-                    if constexpr (F8) umma_commit(sb + C::KFREE);
+                        for (int x = 0; x < C::BLKS * KPB; ++x)
+                            product(tmem + C::QP * N * (s & 1), k + ((x / KPB * C::BLOCK + x % KPB * 32) >> 4),
+                                    q + ((x / KPB * C::QBLOCK + x % KPB * 32) >> 4), id_s, x > 0);
+                        umma_commit(sb + C::SFULL + 8 * (s & 1));
+                    }
+                    __syncwarp();
+                    ++s;
+                    if (++ss == C::STG) { ss = 0; sp ^= 1; }
+                    idle = 0;
+                    continue;
                 }
-                __syncwarp();
-                ++s;
-                if (++ss == C::STG) { ss = 0; sp ^= 1; }
-                idle = 0;
-                continue;
             }
-            go = p < s && mbar_test(sb + C::PFULL, p & 1) && (!F8 || mbar_test(sb + C::VFULL, p & 1));
+            go = p < s && mbar_test(sb + C::PFULL, p & 1);
             if (__all_sync(0xffffffffu, go)) {
                 const bool first = __any_sync(0xffffffffu, meta(p)->flags & kFirst);
                 const int it = item + (first ? 1 : 0);
-                go = !first || it < 2 || mbar_test(sb + C::OFREE + 8 * (it & 1), ((it >> 1) - 1) & 1);
+                go = !first || it < C::OB || mbar_test(sb + C::OFREE + 8 * (it % C::OB), (it / C::OB - 1) & 1);
                 if (__all_sync(0xffffffffu, go)) {
                     item = it;
                     tc_fence_after();
-                    const uint64_t v = v0 + (F8 ? 0 : (uint32_t)(ps * C::STAGE) >> 4);
+                    const uint64_t v = v0 + ((uint32_t)(ps * C::STAGE) >> 4);
                     if (elect_one()) {
 #pragma unroll
-                        for (int x = 0; x < TOK / 16; ++x)
-                            umma_bf16(tmem + 2 * N + N * (it & 1), v + (x * 2048 >> 4), p0 + (x * 256 >> 4), id_o, x > 0 || !first);
+                        for (int x = 0; x < TOK / C::KSTEP; ++x)
+                            product(tmem + 2 * C::QP * N + C::PP * N * (it % C::OB), v + (x * C::KSTEP * C::BROWB >> 4),
+                                    p0 + (x * C::KSTEP * 16 >> 4), id_o, x > 0 || !first);
                         umma_commit(sb + C::PVDONE + 8 * (p & 1));
-                        umma_commit(F8 ? sb + C::VFREE : sb + C::EMPTY + 8 * ps);
+                        umma_commit(sb + C::EMPTY + 8 * ps);
                     }
                     __syncwarp();
                     ++p;
@@ -325,14 +317,15 @@ struct TcKernel {
         // nothing may still run on the tensor pipe when Tensor Memory is released
         if (elect_one()) umma_commit(sb + C::FIN);
         __syncwarp();
-        wait(sb + C::FIN, 0);
+        wait_warp(sb + C::FIN, 0);
     }
 
     // ------------------------------------------------------------------ softmax
     // Four warps have RW rows: wq is the warp among them, row0 the first row, bar their barrier.
-    // This thread's channel of O^T: TMEM lanes are channels, with D = 64 the first 16 of each 32.
+    // This thread's channel of O^T: TMEM lanes are channels, with D = 64 the first 16 of each 32; -1: none.
     static __device__ __forceinline__ int channel(int wq, int lane) { return D == 128 ? 32 * wq + lane : lane < 16 ? 16 * wq + lane : -1; }
-    __device__ __forceinline__ static bool finite16(uint32_t x) { return F8 ? (x & 0x7c00u) != 0x7c00u : (x & 0x7f80u) != 0x7f80u; }
+    typedef typename std::conditional<F8, uint8_t, uint16_t>::type Bits;   // of a value
+    static __device__ __forceinline__ bool finite(uint32_t x) { return F8 ? (x & 0x7fu) != 0x7fu : (x & 0x7f80u) != 0x7f80u; }
     __device__ __forceinline__ bool sees(const Meta& mt, int j, int p) const {
         return (j <= p) & (j >= mt.start) & ((P.window <= 0) | ((int64_t)p - j < P.window));
     }
@@ -343,50 +336,67 @@ struct TcKernel {
     // All softmax warps.
     __device__ __forceinline__ void sanitize(const Meta& mt, int t, bool ok, int wq, int lane, int row0, uint32_t& pos, uint32_t& neg) {
         constexpr uint32_t ALL = 32 * C::SW;
-        uint8_t* v = sm + (v_image(t) - sb);
+        uint8_t* v = v_image(t);
         const int key = 32 * wq + lane, j = mt.j0 + key;
         uint32_t bad = 0;
         if (ok && (j > mt.pos0 || j < mt.all_lo)) {
 #pragma unroll
-            for (int h = 0; h < D / 64; ++h)
+            for (int ch = 0; ch < C::ROWB / 16; ++ch) {
+                const uint4 u = *reinterpret_cast<const uint4*>(v + C::chunk(key, ch));
+                const uint32_t a[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                for (int ch = 0; ch < 8; ++ch) {
-                    const uint4 u = *reinterpret_cast<const uint4*>(v + h * C::HALF + sm100::sw128_off(key, ch));
-                    const uint32_t a[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) bad |= !finite16(a[x] & 0xffffu) | !finite16(a[x] >> 16);
+                for (int x = 0; x < 4; ++x) {
+                    bad |= !finite(a[x] & 0xffffu) | !finite(a[x] >> 16);
+                    if (F8) bad |= !finite(a[x] >> 8 & 0xffu) | !finite(a[x] >> 24);
                 }
+            }
         }
         if (!bar_any(3, bad != 0, ALL)) return;
         volatile uint32_t* bits = reinterpret_cast<volatile uint32_t*>(sm + C::BITS);
         const uint32_t mine = __ballot_sync(0xffffffffu, bad != 0);
         if (lane == 0) bits[wq] = mine;   // the same of both groups of warps
-        sm100::named_bar(3, ALL);
+        bar_all(3, ALL);
         const int d = channel(wq, lane);
         auto element = [&](int k) {
-            return reinterpret_cast<uint16_t*>(v + (d >> 6) * C::HALF + sm100::sw128_off(k, (d & 63) >> 3) + 2 * (d & 7));
+            const int byte = d * (int)sizeof(Bits);
+            return reinterpret_cast<Bits*>(v + C::chunk(k, byte >> 4) + (byte & 15));
         };
         if (d >= 0)
             for (int x = 0; x < 4; ++x)
                 for (uint32_t m = bits[x]; m; m &= m - 1) {
                     const int k = 32 * x + __ffs(m) - 1;
                     const uint32_t val = *element(k);
-                    if (finite16(val)) continue;
-                    const bool nan = F8 ? (val & 0x3ffu) != 0 : (val & 0x7fu) != 0, minus = val & 0x8000u;
+                    if (finite(val)) continue;
+                    const bool nan = F8 || (val & 0x7fu) != 0, minus = val & 0x8000u;   // e4m3 has no infinities
                     for (int r = 0; r < C::RW && row0 + r < mt.rows; ++r) {
                         if (!sees(mt, mt.j0 + k, mt.pos0 + (mt.block * N + row0 + r) / P.group)) continue;
                         if (nan || !minus) pos |= 1u << r;
                         if (nan || minus) neg |= 1u << r;
                     }
                 }
-        sm100::named_bar(3, ALL);   // all have read
+        bar_all(3, ALL);   // all have read
         if (d >= 0 && row0 == 0)
             for (int x = 0; x < 4; ++x)
                 for (uint32_t m = bits[x]; m; m &= m - 1) {
-                    uint16_t* e = element(32 * x + __ffs(m) - 1);
-                    if (!finite16(*e)) *e = 0;
+                    Bits* e = element(32 * x + __ffs(m) - 1);
+                    if (!finite(*e)) *e = 0;
                 }
-        sm100::named_bar(3, ALL);   // the list may be written again
+        bar_all(3, ALL);   // the list may be written again
+    }
+
+    // 8 rows of O^T, the parts summed up
+    static __device__ __forceinline__ void load_out(uint32_t t, float (&o)[8]) {
+        tmem_ld8(t, o);
+        if constexpr (F8) {
+            float b[8], c[8];
+            tmem_ld8(t + N, b);
+            tmem_ld8(t + 2 * N, c);
+            sm100::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] += (b[i] + c[i] * (1.f / 16)) * (1.f / 16);
+        } else {
+            sm100::tmem_wait_ld();
+        }
     }
 
     __device__ __forceinline__ void softmax(uint32_t tmem, int w, int lane) {
@@ -403,12 +413,12 @@ struct TcKernel {
         uint32_t pos = 0, neg = 0;
         bool bad = false;
         for (int t = 0; t < T; ++t) {
-            bad = bad || !wait(sb + C::MFULL + 8 * (t % C::MD), (t / C::MD) & 1);
+            bad |= !wait_warp(sb + C::MFULL + 8 * (t % C::MD), (t / C::MD) & 1);
             const Meta mt = *meta(t);
             const bool first = mt.flags & kFirst, edge = mt.flags & kEdge;
-            const int rows = mt.rows - row0;   // of these warps; maybe none
+            const int rows = min(mt.rows - row0, RW);   // of these warps; maybe none
             if (first) {
-                if constexpr (F8) bad = bad || !wait(sb + C::QFULL + 8 * (mt.item & 1), (mt.item >> 1) & 1);
+                if constexpr (F8) bad |= !wait_warp(sb + C::QFULL + 8 * (mt.item % C::QS), (mt.item / C::QS) & 1);
                 if (tid < RW) {
                     mrow[tid] = make_float2(-INFINITY, 0.f);
                     float f = P.scale * (P.softcap > 0.f ? 2.f * kLog2e / P.softcap : kLog2e), slope = 0.f;
@@ -420,12 +430,12 @@ struct TcKernel {
                 for (int r = 0; r < RW; ++r) l[r] = 0.f;
                 pos = neg = 0;
             }
-            bad = bad || !wait(sb + C::SFULL + 8 * (t & 1), (t >> 1) & 1);
+            bad |= !wait_warp(sb + C::SFULL + 8 * (t & 1), (t >> 1) & 1);
             if (bar_any(bar, bad || aborted(), 128)) break;
             tc_fence_after();
             const bool ok = (reinterpret_cast<const uint32_t*>(sm + C::OKM + (t % C::MD) * 16)[wq] >> lane) & 1;
             const bool mask = edge || !__all_sync(0xffffffffu, ok);
-            const uint32_t tS = tl + N * (t & 1) + row0, tO = tl + 2 * N + N * (mt.item & 1) + row0;
+            const uint32_t tS = tl + C::QP * N * (t & 1) + row0, tO = tl + 2 * C::QP * N + C::PP * N * (mt.item % C::OB) + row0;
             const int j = mt.j0 + key;
             float s[RW];
             if (rows > 0) {
@@ -442,6 +452,13 @@ struct TcKernel {
 #pragma unroll
             for (int c = 0; c < RW; c += 8) {
                 if (c >= rows) break;
+                if constexpr (F8) {   // the product with the queries' second part
+                    float s2[8];
+                    tmem_ld8(tS + N + c, s2);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) s[c + i] += s2[i] * (1.f / 16);
+                }
                 float2 in[8];
                 float top[8];
 #pragma unroll
@@ -477,7 +494,7 @@ struct TcKernel {
                 for (int i = 0; i < 8; ++i) up |= s[c + i] > top[i];
             }
             // the weights of the tile before, and O, are free
-            if (t > 0) bad = bad || !wait(sb + C::PVDONE + 8 * ((t - 1) & 1), ((t - 1) >> 1) & 1);
+            if (t > 0) bad |= !wait_warp(sb + C::PVDONE + 8 * ((t - 1) & 1), ((t - 1) >> 1) & 1);
             if (bar_any(bar, up != 0, 128)) {
                 // some row's maximum rises: the new one, and what the sums so far are worth in it
                 tc_fence_after();
@@ -492,32 +509,33 @@ struct TcKernel {
                     }
                 }
                 if (lane < RW) wred[wq * N + lane] = mine;
-                named_bar(bar, 128);
+                bar_all(bar, 128);
                 if (tid < RW) {
                     const float top = fmaxf(fmaxf(wred[tid], wred[N + tid]), fmaxf(wred[2 * N + tid], wred[3 * N + tid]));
                     const float2 old = mrow[tid];
                     float f = 1.f;
                     if (top > old.x) {
-                        f = old.x == -INFINITY ? 0.f : ex2(old.y - top);
-                        mrow[tid] = make_float2(top + kSlack, top);
+                        f = old.x == -INFINITY ? 0.f : ex2(old.y + C::BASE - top);
+                        mrow[tid] = make_float2(top + C::SLACK, top - C::BASE);
                     }
                     frow[tid] = f;
                 }
-                named_bar(bar, 128);
+                bar_all(bar, 128);
                 if (!first) {
 #pragma unroll
                     for (int c = 0; c < RW; c += 8) {
                         if (c >= rows) break;
-                        float o[8];
-                        tmem_ld8(tO + c, o);
-                        tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float f = frow[c + i];
-                            l[c + i] *= f;
-                            o[i] *= f;
+                        for (int i = 0; i < 8; ++i) l[c + i] *= frow[c + i];
+#pragma unroll
+                        for (int y = 0; y < C::PP; ++y) {
+                            float o[8];
+                            tmem_ld8(tO + y * N + c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) o[i] *= frow[c + i];
+                            tmem_st8(tO + y * N + c, o);
                         }
-                        tmem_st8(tO + c, o);
                     }
                     tmem_wait_st();
                 }
@@ -525,26 +543,43 @@ struct TcKernel {
 #pragma unroll
             for (int c = 0; c < RW; c += 8) {
                 if (c >= rows) break;
-                uint32_t pk[4];
+                uint32_t pk[4], part[3][2] = {};
 #pragma unroll
                 for (int i = 0; i < 8; i += 2) {
                     const float4 m = *reinterpret_cast<const float4*>(mrow + c + i);
                     const float a = ex2(s[c + i] - m.y), b = ex2(s[c + i + 1] - m.w);
                     l[c + i] += a;
                     l[c + i + 1] += b;
-                    pk[i / 2] = F8 ? pack_half2(a, b) : pack_bf16x2(a, b);
-                }
-                *reinterpret_cast<uint4*>(sm + C::PM + ((row0 + c) / 8) * (TOK * 16) + key * 16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-            }
-            if (!F8 && !ok && row0 == 0) {   // a value row that was not fetched
-                bad = bad || !wait(full_bar(t), full_phase(t));
-                uint8_t* v = sm + (v_image(t) - sb);
+                    if constexpr (F8) {   // remainders are exact: fp16 has 11 bits, each part takes 4 and the sign
+                        const __half2 k16 = __float2half2_rn(16.f);
+                        __half2 r = __floats2half2_rn(a, b);
 #pragma unroll
-                for (int x = 0; x < D / 8; ++x)
-                    *reinterpret_cast<uint4*>(v + (x >> 3) * C::HALF + sm100::sw128_off(key, x & 7)) = make_uint4(0u, 0u, 0u, 0u);
+                        for (int y = 0; y < 3; ++y) {
+                            const uint32_t e = e4m3x2(r);
+                            part[y][i / 4] |= e << (16 * (i / 2 % 2));
+                            if (y < 2) r = __hmul2(__hsub2(r, half2_of(e)), k16);
+                        }
+                    } else {
+                        pk[i / 2] = pack_bf16x2(a, b);
+                    }
+                }
+                uint8_t* at = sm + C::PM + (row0 + c) / C::PG * (TOK * 16) + key * 16;
+                if constexpr (F8) {
+#pragma unroll
+                    for (int y = 0; y < 3; ++y)
+                        *reinterpret_cast<uint2*>(at + y * (N / 16) * (TOK * 16) + c % 16) = make_uint2(part[y][0], part[y][1]);
+                } else {
+                    *reinterpret_cast<uint4*>(at) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                }
+            }
+            if (!ok && row0 == 0) {   // a value row that was not fetched, or that no token sees
+                bad |= !wait_full(t);
+#pragma unroll
+                for (int ch = 0; ch < C::ROWB / 16; ++ch) *reinterpret_cast<uint4*>(v_image(t) + C::chunk(key, ch)) = make_uint4(0u, 0u, 0u, 0u);
             }
             if (edge && mt.nq > 1) {
-                bad = bad || !wait(F8 ? sb + C::VFULL : full_bar(t), F8 ? t & 1 : full_phase(t));
+                bad |= !wait_full(t);
+                __syncwarp();
                 sanitize(mt, t, ok, wq, lane, row0, pos, neg);
             }
             tc_fence_before();
@@ -575,7 +610,7 @@ struct TcKernel {
                     }
                 if (lane < 16) wred[wq * N + 16 * x + lane] = v[0];
             }
-            named_bar(bar, 128);
+            bar_all(bar, 128);
             float sum = 0.f, top = 0.f;
             if (tid < rows) {
                 sum = wred[tid] + wred[N + tid] + wred[2 * N + tid] + wred[3 * N + tid];
@@ -584,8 +619,8 @@ struct TcKernel {
                 const float vs = F8 && P.c.v_scale ? P.c.v_scale[mt.h] : 1.f;
                 frow[tid] = mt.part >= 0 ? 1.f : sum == 0.f ? 0.f : vs / sum;
             }
-            named_bar(bar, 128);
-            bad = bad || !wait(sb + C::PVDONE + 8 * (t & 1), (t >> 1) & 1);
+            bar_all(bar, 128);
+            bad |= !wait_warp(sb + C::PVDONE + 8 * (t & 1), (t >> 1) & 1);
             tc_fence_after();
             const int d = channel(wq, lane);
             tok = mt.tok0;
@@ -602,8 +637,7 @@ struct TcKernel {
                 for (int c = 0; c < RW; c += 8) {
                     if (c >= rows) break;
                     float o[8];
-                    tmem_ld8(tO + c, o);
-                    tmem_wait_ld();
+                    load_out(tO + c, o);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         float x = o[i];
@@ -620,8 +654,7 @@ struct TcKernel {
                 for (int c = 0; c < RW; c += 8) {
                     if (c >= rows) break;
                     float o[8];
-                    tmem_ld8(tO + c, o);
-                    tmem_wait_ld();
+                    load_out(tO + c, o);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         float x = o[i];
@@ -633,7 +666,7 @@ struct TcKernel {
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(sb + C::OFREE + 8 * (mt.item & 1));
+            if (lane == 0) mbar_arrive(sb + C::OFREE + 8 * (mt.item % C::OB));
             if (tid < rows) {
                 if (mt.part >= 0) {
                     to[tid] = top;
@@ -649,6 +682,7 @@ struct TcKernel {
 
     __device__ __forceinline__ void run() {
         const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+        if (tid == 0) { prefetch_map(&P.k_map); prefetch_map(&P.v_map); prefetch_map(&P.q_map); }
         W w(P);
         w.template find<C::THREADS>(reinterpret_cast<int64_t*>(sm + C::RING));
         kda_grid_launch_next();
@@ -661,17 +695,11 @@ struct TcKernel {
         if (tid == 32) {
             for (int i = 0; i < C::STG; ++i) {
                 sm100::mbar_init(sb + C::FULL + 8 * i, 1);
-                sm100::mbar_init(sb + C::EMPTY + 8 * i, F8 ? C::LW : 1);
+                sm100::mbar_init(sb + C::EMPTY + 8 * i, 1);
+                sm100::mbar_init(sb + C::QRAW + 8 * i, 1);
+                sm100::mbar_init(sb + C::QFULL + 8 * i, F8 ? C::LW : 1);
             }
             for (int i = 0; i < C::MD; ++i) sm100::mbar_init(sb + C::MFULL + 8 * i, 1);
-            if (F8) {
-                sm100::mbar_init(sb + C::KFULL, C::LW);
-                sm100::mbar_init(sb + C::KFREE, 1);
-                sm100::mbar_init(sb + C::VFULL, C::LW);
-                sm100::mbar_init(sb + C::VFREE, 1);
-                sm100::mbar_init(sb + C::QFULL, C::LW);
-                sm100::mbar_init(sb + C::QFULL + 8, C::LW);
-            }
             for (int i = 0; i < 2; ++i) {
                 sm100::mbar_init(sb + C::SFULL + 8 * i, 1);
                 sm100::mbar_init(sb + C::SFREE + 8 * i, C::SW);
@@ -694,7 +722,7 @@ struct TcKernel {
         } else if (warp == C::SW + 1) {
             issuer(tmem);
         } else {
-            if constexpr (F8) converter(warp - C::SW - 2, lane);
+            if constexpr (F8) splitter(warp - C::SW - 2, lane);
         }
         sm100::tc_fence_before();
         __syncthreads();
