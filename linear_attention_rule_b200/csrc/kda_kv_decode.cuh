@@ -180,9 +180,13 @@ struct Meta {
     int32_t pad;
 };
 static_assert(sizeof(Meta) == 64, "laid out in shared memory");
-enum : int32_t { kFirst = 1, kLast = 2, kEdge = 4 };   // first, last tile of the item here; not all keys seen by all
+enum : int32_t { kFirst = 1, kLast = 2, kEdge = 4, kEnd = 8 };   // first, last tile of the item here; not all keys seen by all; last tile of all
 
-// The stretch of tiles of this worker, and the walk along it.
+// The stretch of this worker, and the walk along its tiles.  An item takes a unit of the line for each of
+// its tiles and, before them, kItemCost for its beginning and end (queries, the first maximum, the
+// outputs): with as many tiles a stretch of short sequences took three times as long as others.
+constexpr int kItemCost = 2;
+
 template <int TOK, int ROWS>
 struct Walk {
     const Params& P;
@@ -192,6 +196,7 @@ struct Walk {
     Seq s;
     int h, block, tile, tiles, i;   // the item here: its tiles [tile, tile + tiles), the i-th of them is next
     bool starts, ends;              // whether it begins and ends in this stretch
+    bool more;                      // whether another item has tiles here
 
     __device__ __forceinline__ explicit Walk(const Params& p) : P(p) {}
 
@@ -212,7 +217,7 @@ struct Walk {
             if (x < slice && gr < groups)
                 for (int m = gr * per_group; m < min(N, (gr + 1) * per_group); ++m) {
                     const Seq q = seq_info<TOK>(P, m, ROWS);
-                    mine[x] += (int64_t)q.tiles * q.blocks * P.c.Hkv;
+                    mine[x] += units(q) * q.blocks * P.c.Hkv;
                 }
             sum += mine[x];
         }
@@ -249,17 +254,22 @@ struct Walk {
         item = -1;
         __syncthreads();
     }
-    // The item that holds `at` < end.
-    __device__ __forceinline__ void seek() {
+    // Units of an item of a sequence.
+    static __device__ __forceinline__ int64_t units(const Seq& q) { return q.tiles + kItemCost; }
+    // The item that holds `at`; false if nothing of its tiles lies in the stretch.
+    __device__ __forceinline__ bool seek() {
+        if (at >= end) return false;
         int64_t items = (int64_t)s.blocks * P.c.Hkv;
-        while (at - base >= items * s.tiles) {
-            base += items * s.tiles;
+        while (at - base >= items * units(s)) {
+            base += items * units(s);
             ++n;
             s = seq_info<TOK>(P, n, ROWS);
             items = (int64_t)s.blocks * P.c.Hkv;
         }
-        const int x = quotient(at - base, s.tiles);
-        const int64_t a = base + (int64_t)x * s.tiles, b = a + s.tiles;
+        const int x = quotient(at - base, units(s));
+        const int64_t a = base + x * units(s) + kItemCost, b = a + s.tiles;   // its tiles
+        at = max(at, a);
+        if (at >= end) return false;
         h = x / s.blocks;
         block = x - h * s.blocks;
         rows = min(ROWS, s.nq * P.group - block * ROWS);
@@ -267,11 +277,13 @@ struct Walk {
         all_lo = first_key(P, s.start, s.pos0 + s.nq - 1);
         tile = s.tile0 + (int)(at - a);
         tiles = (int)(min(b, end) - at);
-        starts = a >= begin;
+        starts = at == a;
         ends = b <= end;
+        more = end - b > kItemCost;
         last_worker = quotient(b - 1, per);
         i = 0;
         ++item;
+        return true;
     }
     int last_worker, rows, tok0, all_lo;
 
@@ -281,16 +293,16 @@ struct Walk {
     }
 
     __device__ __forceinline__ int j0() const { return (tile + i) * TOK; }
-    __device__ __forceinline__ void next() {
+    __device__ __forceinline__ bool next() {
         ++at;
-        if (++i == tiles && at < end) seek();
+        return ++i < tiles || seek();
     }
     __device__ __forceinline__ void fill(Meta* m) const {
         const int j = j0();
         const bool inside = j >= all_lo && j + TOK - 1 <= min(s.pos0, s.hi - 1);
         m->t0 = s.t0;
         m->j0 = j;
-        m->flags = (i == 0 ? kFirst : 0) | (i == tiles - 1 ? kLast : 0) | (inside ? 0 : kEdge);
+        m->flags = (i == 0 ? kFirst : 0) | (i == tiles - 1 ? kLast | (more ? 0 : kEnd) : 0) | (inside ? 0 : kEdge);
         m->h = h;
         m->block = block;
         m->rows = rows;
@@ -361,7 +373,7 @@ struct Fetch {
             sm100::mbar_arrive(meta_bar);
             const uint32_t queries = w.i == 0 ? C::QB : 0;
             sm100::mbar_arrive_expect_tx(bar, boxes * (uint32_t)(2 * box * C::ROWB) + (qbar == bar ? queries : 0));
-            if (qbar != bar && queries) *last = w.at + w.tiles >= w.end;
+            if (qbar != bar && queries) *last = !w.more;
             if (qbar != bar && queries) sm100::mbar_arrive_expect_tx(qbar, queries);
         }
         __syncwarp();
@@ -388,25 +400,26 @@ struct Fetch {
             }
         }
     }
-    // The whole stretch of T tiles.  free(t): waits until stage, queries and meta of tile t may be
-    // overwritten; at(t): where they are.
-    template <typename Free, typename Put>
-    __device__ __forceinline__ bool run(W& w, int T, Free free, Put at) {
+    // Finds the first tile; false if the stretch has none.
+    __device__ __forceinline__ bool begin(W& w) {
         if (lane == 0) P.split[blockIdx.x].last = -1;
         w.s = seq_info<C::TOK>(P, w.n, ROWS);
-        w.seek();
+        if (!w.seek()) return false;
         if (lane == 0) w.tell_join(P.split + blockIdx.x);
         look(w);
-        for (int t = 0; t < T; ++t) {
+        return true;
+    }
+    // Tiles from the one that the walk stands at.  free(t): waits until stage, queries and meta of tile t
+    // may be overwritten; at(t): puts it there.
+    template <typename Free, typename Put>
+    __device__ __forceinline__ bool run(W& w, Free free, Put at) {
+        for (int t = 0;; ++t) {
             if (!free(t)) return false;
             at(t);
-            if (t + 1 < T) {
-                w.next();
-                if (w.i == 0 && lane == 0) w.tell_join(P.split + blockIdx.x);
-                look(w);
-            }
+            if (!w.next()) return true;
+            if (w.i == 0 && lane == 0) w.tell_join(P.split + blockIdx.x);
+            look(w);
         }
-        return true;
     }
 };
 

@@ -39,7 +39,6 @@ struct SimtKernel {
     const Params& P;
     uint8_t* sm;
     uint32_t sb;
-    int T;
 
     __device__ __forceinline__ Meta* meta(int t) const { return reinterpret_cast<Meta*>(sm + C::META) + t % C::MD; }
     __device__ __forceinline__ void fail() const {
@@ -48,21 +47,23 @@ struct SimtKernel {
     }
     __device__ __forceinline__ bool aborted() const { return *reinterpret_cast<volatile uint32_t*>(sm + C::ABORT) != 0; }
 
-    __device__ __forceinline__ void fetcher(W& w, int lane) {
-        Fetch<C, R> f{P, lane, {}};
+    __device__ __forceinline__ void fetcher(Fetch<C, R>& f, W& w) {
+        int puts = 0;
         const bool ok = f.run(
-            w, T,
+            w,
             [&](int t) {
                 return !aborted() && (t < C::STG || wait_warp(sb + C::EMPTY + 8 * (t % C::STG), (t / C::STG - 1) & 1));
             },
             [&](int t) {
                 f.put(w, sb + (t % C::STG) * C::STAGE, sb + C::Q + (w.item % C::QS) * C::QB, sb + C::FULL + 8 * (t % C::STG),
-                      sb + C::FULL + 8 * (t % C::STG), sb + C::MFULL + 8 * (t % C::MD), meta(t), reinterpret_cast<uint32_t*>(sm + C::OKM + (t % C::MD) * 16), nullptr);
+                      sb + C::FULL + 8 * (t % C::STG), sb + C::MFULL + 8 * (t % C::MD), meta(t),
+                      reinterpret_cast<uint32_t*>(sm + C::OKM + (t % C::MD) * 16), nullptr);
+                puts = t + 1;
             });
-        if (!ok) fail();
-        // copies still in flight at the end of an aborted run
-        if (aborted())
-            for (int t = max(T - C::STG, 0); t < T; ++t) wait(sb + C::FULL + 8 * (t % C::STG), (t / C::STG) & 1);
+        if (!ok) {   // copies still in flight are waited for
+            fail();
+            for (int t = max(puts - C::STG, 0); t < puts; ++t) wait_warp(sb + C::FULL + 8 * (t % C::STG), (t / C::STG) & 1);
+        }
     }
 
     // byte offset of 16-byte chunk ch of a key's row
@@ -77,7 +78,7 @@ struct SimtKernel {
         const int d = tid % D, kg = tid / D;
         float acc[R], m = -INFINITY, l = 0.f;   // m, l: of row w
         bool bad = false;
-        for (int t = 0; t < T; ++t) {
+        for (int t = 0;; ++t) {
             bad |= !wait_warp(sb + C::FULL + 8 * (t % C::STG), (t / C::STG) & 1);
             if (bar_any(1, bad || aborted(), NT)) break;
             const Meta mt = *meta(t);
@@ -202,6 +203,7 @@ struct SimtKernel {
                         if (c == 0) { to[r] = ml[r]; to[R + r] = sum; }
                     }
                 }
+                if (mt.flags & kEnd) break;
             }
         }
         if (bad) fail();
@@ -213,30 +215,31 @@ struct SimtKernel {
         W w(P);
         w.template find<C::THREADS>(reinterpret_cast<int64_t*>(sm));
         kda_grid_launch_next();
-        T = (int)(w.end - w.begin);
-        if (T == 0) {
-            if (tid == 0) P.split[blockIdx.x].last = -1;
-            return;
-        }
-        if (tid == 0) {
-            for (int i = 0; i < C::STG; ++i) {
-                sm100::mbar_init(sb + C::FULL + 8 * i, 1);
-                sm100::mbar_init(sb + C::EMPTY + 8 * i, C::CW);
+        Fetch<C, R> f{P, lane, {}};
+        if (warp == C::CW) {
+            if (lane == 0) {
+                for (int i = 0; i < C::STG; ++i) {
+                    sm100::mbar_init(sb + C::FULL + 8 * i, 1);
+                    sm100::mbar_init(sb + C::EMPTY + 8 * i, C::CW);
+                }
+                for (int i = 0; i < C::MD; ++i) sm100::mbar_init(sb + C::MFULL + 8 * i, 1);
+                sm100::fence_mbar_init();
             }
-            for (int i = 0; i < C::MD; ++i) sm100::mbar_init(sb + C::MFULL + 8 * i, 1);
-            sm100::fence_mbar_init();
-            *reinterpret_cast<volatile uint32_t*>(sm + C::ABORT) = 0;
+            const bool any = f.begin(w);
+            if (lane == 0) *reinterpret_cast<volatile uint32_t*>(sm + C::ABORT) = 0;
+            if (lane == 0) *reinterpret_cast<volatile uint32_t*>(sm + C::ABORT + 4) = any;
         }
         __syncthreads();
+        if (!*reinterpret_cast<volatile uint32_t*>(sm + C::ABORT + 4)) return;
         if (warp < C::CW) consumer(warp, lane);
-        else fetcher(w, lane);
+        else fetcher(f, w);
     }
 };
 
 template <int D, int R>
 __global__ void __launch_bounds__(Simt<D, R>::THREADS, 1) attend_simt_kernel(const __grid_constant__ Params P) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    SimtKernel<D, R> k{P, smem, sm100::smem_u32(smem), 0};
+    SimtKernel<D, R> k{P, smem, sm100::smem_u32(smem)};
     k.run();
 }
 

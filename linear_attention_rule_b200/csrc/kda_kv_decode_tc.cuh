@@ -9,8 +9,8 @@
 // as one 16-byte chunk per 8 rows (P MN-major without swizzle, free of bank conflicts).  Only the
 // running maximum is shared, and the tile that raises it by more than 2^8 is rare (kSlack).
 //
-// Warps: 4 for softmax and epilogue (TMEM lanes 32 w ..) for every 16 rows (8 with 32 and 64), which
-// share nothing but keys and values; then one that fetches tiles, one that issues the products, and
+// Warps: 4 for softmax and epilogue (TMEM lanes 32 w ..) for every 8 rows (16 of 64), which share
+// nothing but keys and values; then one that fetches tiles, one that issues the products, and
 // with an e4m3 cache four that split queries.  S and O are double-buffered in TMEM, so the product
 // of the next tile runs during the softmax of this one and the next item starts during the epilogue
 // of the last.  Tiles land in the operand images directly: TMA's swizzle is the images'.
@@ -37,7 +37,7 @@ struct Tc {
     static constexpr int D = D_;
     static constexpr bool F8 = sizeof(TC) == 1;
     static constexpr int TOK = 128;
-    static constexpr int SW = N >= 32 ? 8 : 4, RW = N / (SW / 4);             // softmax warps, rows of four of them
+    static constexpr int RW = N == 64 ? 16 : 8, SW = 4 * N / RW;              // rows of four softmax warps, softmax warps
     static constexpr int LW = F8 ? 4 : 0;                                     // splitting warps
     static constexpr int THREADS = 32 * (SW + 2 + LW);
     static constexpr int QP = F8 ? 2 : 1, PP = F8 ? 3 : 1;                    // parts of queries and weights
@@ -141,11 +141,12 @@ struct TcKernel {
     typedef Walk<C::TOK, N> W;
     static constexpr bool F8 = C::F8;
     static constexpr int TOK = C::TOK;
+    // named barriers: 1 .. of the groups of softmax warps, of all of them, of the splitting warps
+    static constexpr uint32_t kAllBar = 1 + C::SW / 4, kSplitBar = 2 + C::SW / 4;
 
     const Params& P;
     uint8_t* sm;
     uint32_t sb;
-    int T;   // tiles of this stretch
 
     __device__ __forceinline__ Meta* meta(int t) const { return reinterpret_cast<Meta*>(sm + C::META) + t % C::MD; }
     __device__ __forceinline__ void fail() const {
@@ -155,23 +156,26 @@ struct TcKernel {
     __device__ __forceinline__ bool aborted() const { return *reinterpret_cast<volatile uint32_t*>(sm + C::ABORT) != 0; }
 
     // ------------------------------------------------------------------ fetching
-    __device__ __forceinline__ void fetcher(W& w, int lane) {
-        Fetch<C, N> f{P, lane, {}};
+    __device__ __forceinline__ void put(Fetch<C, N>& f, const W& w, int t) {
+        f.put(w, sb + C::RING + (t % C::STG) * C::STAGE, sb + C::Q + (w.item % C::QS) * C::QB, sb + C::FULL + 8 * (t % C::STG),
+              F8 ? sb + C::QRAW + 8 * (w.item % C::QS) : sb + C::FULL + 8 * (t % C::STG), sb + C::MFULL + 8 * (t % C::MD), meta(t),
+              reinterpret_cast<uint32_t*>(sm + C::OKM + (t % C::MD) * 16), reinterpret_cast<uint32_t*>(sm + C::QLAST) + w.item % C::QS);
+    }
+    __device__ __forceinline__ void fetcher(Fetch<C, N>& f, W& w) {
+        int puts = 0;
         const bool ok = f.run(
-            w, T,
+            w,
             [&](int t) {
                 return !aborted() && (t < C::STG || wait_warp(sb + C::EMPTY + 8 * (t % C::STG), (t / C::STG - 1) & 1));
             },
             [&](int t) {
-                f.put(w, sb + C::RING + (t % C::STG) * C::STAGE, sb + C::Q + (w.item % C::QS) * C::QB, sb + C::FULL + 8 * (t % C::STG),
-                      F8 ? sb + C::QRAW + 8 * (w.item % C::QS) : sb + C::FULL + 8 * (t % C::STG), sb + C::MFULL + 8 * (t % C::MD), meta(t), reinterpret_cast<uint32_t*>(sm + C::OKM + (t % C::MD) * 16),
-                      reinterpret_cast<uint32_t*>(sm + C::QLAST) + w.item % C::QS);
+                put(f, w, t);
+                puts = t + 1;
             });
-        if (!ok) fail();
-    }
-    // Copies in flight at the end of an aborted run are waited for (a fetch of a whole tile each).
-    __device__ __forceinline__ void drain() {
-        for (int t = max(T - C::STG, 0); t < T; ++t) wait(sb + C::FULL + 8 * (t % C::STG), (t / C::STG) & 1);
+        if (!ok) {   // copies still in flight are waited for
+            fail();
+            for (int t = max(puts - C::STG, 0); t < puts; ++t) wait_warp(sb + C::FULL + 8 * (t % C::STG), (t / C::STG) & 1);
+        }
     }
 
     // ------------------------------------------------------------------ queries in two e4m3 parts
@@ -193,9 +197,10 @@ struct TcKernel {
 #pragma unroll
             for (int o = LANES / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             const int ex = (int)((__float_as_uint(top) >> 23) & 255u);
-            const int sh = ex == 0 || ex == 255 ? 0 : ex - 127 - 7;
+            const int sh = ex == 0 || ex == 255 ? 0 : max(ex - 127 - 7, -126);
+            const float down = __uint_as_float((uint32_t)(127 - sh) << 23);   // 2^-sh, exact
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = ex == 255 ? x[e] - x[e] : scalbnf(x[e], -sh);   // a row with an infinity scores NaN
+            for (int e = 0; e < 4; ++e) x[e] = ex == 255 ? x[e] - x[e] : x[e] * down;   // a row with an infinity scores NaN
             uint32_t a = 0, b = 0;
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {
@@ -206,9 +211,9 @@ struct TcKernel {
             }
             one[it] = a;
             two[it] = b;
-            if (sub == 0) reinterpret_cast<float*>(sm + C::QF)[slot * N + r] = scalbnf(1.f, sh);
+            if (sub == 0) reinterpret_cast<float*>(sm + C::QF)[slot * N + r] = __uint_as_float((uint32_t)(127 + sh) << 23);
         }
-        bar_all(4, 32 * C::LW);
+        bar_all(kSplitBar, 32 * C::LW);
 #pragma unroll
         for (int it = 0; it < ITER; ++it) {
             const int r = (it * C::LW + lw) * RPI + lane / LANES;
@@ -225,7 +230,7 @@ struct TcKernel {
         for (int item = 0;; ++item) {
             const int slot = item % C::QS;
             ok = wait_warp(sb + C::QRAW + 8 * slot, (item / C::QS) & 1);
-            if (bar_any(4, !ok || aborted(), 32 * C::LW)) break;
+            if (bar_any(kSplitBar, !ok || aborted(), 32 * C::LW)) break;
             const bool last = reinterpret_cast<const uint32_t*>(sm + C::QLAST)[slot];
             split_queries(slot, lw, lane);
             sm100::fence_proxy_async_smem();
@@ -259,9 +264,9 @@ struct TcKernel {
         uint32_t sp = 0;                     // phase of tile s's stage
         int qitem = -1, qslot = -1, item = -1;   // of tile s, of tile p
         long long t0 = 0;
-        bool ok = true;
-        for (uint32_t idle = 0; p < T;) {
-            bool go = s < T && s < p + 2 && mbar_test(sb + C::FULL + 8 * ss, sp) &&
+        bool ok = true, more = true, done = false;   // more scores to come, all done
+        for (uint32_t idle = 0; !done;) {
+            bool go = more && s < p + 2 && mbar_test(sb + C::FULL + 8 * ss, sp) &&
                       (s < 2 || mbar_test(sb + C::SFREE + 8 * (s & 1), ((s >> 1) - 1) & 1));
             if (__all_sync(0xffffffffu, go)) {
                 const bool first = __any_sync(0xffffffffu, meta(s)->flags & kFirst);
@@ -280,6 +285,7 @@ struct TcKernel {
                         umma_commit(sb + C::SFULL + 8 * (s & 1));
                     }
                     __syncwarp();
+                    more = !__any_sync(0xffffffffu, meta(s)->flags & kEnd);
                     ++s;
                     if (++ss == C::STG) { ss = 0; sp ^= 1; }
                     idle = 0;
@@ -304,6 +310,7 @@ struct TcKernel {
                         umma_commit(sb + C::EMPTY + 8 * ps);
                     }
                     __syncwarp();
+                    done = __any_sync(0xffffffffu, meta(p)->flags & kEnd);
                     ++p;
                     if (++ps == C::STG) ps = 0;
                     idle = 0;
@@ -327,7 +334,7 @@ struct TcKernel {
     typedef typename std::conditional<F8, uint8_t, uint16_t>::type Bits;   // of a value
     static __device__ __forceinline__ bool finite(uint32_t x) { return F8 ? (x & 0x7fu) != 0x7fu : (x & 0x7f80u) != 0x7f80u; }
     __device__ __forceinline__ bool sees(const Meta& mt, int j, int p) const {
-        return (j <= p) & (j >= mt.start) & ((P.window <= 0) | ((int64_t)p - j < P.window));
+        return (j <= p) & (j >= mt.start) & ((P.window <= 0) | (p - j < P.window));
     }
 
     // Keys that some tokens see and some do not take part in the product for all (with weight 0
@@ -345,17 +352,15 @@ struct TcKernel {
                 const uint4 u = *reinterpret_cast<const uint4*>(v + C::chunk(key, ch));
                 const uint32_t a[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    bad |= !finite(a[x] & 0xffffu) | !finite(a[x] >> 16);
-                    if (F8) bad |= !finite(a[x] >> 8 & 0xffu) | !finite(a[x] >> 24);
-                }
+                for (int x = 0; x < 4; ++x)   // all ones in a field carry out of it
+                    bad |= F8 ? ((a[x] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u : ((a[x] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
             }
         }
-        if (!bar_any(3, bad != 0, ALL)) return;
+        if (!bar_any(kAllBar, bad != 0, ALL)) return;
         volatile uint32_t* bits = reinterpret_cast<volatile uint32_t*>(sm + C::BITS);
         const uint32_t mine = __ballot_sync(0xffffffffu, bad != 0);
         if (lane == 0) bits[wq] = mine;   // the same of both groups of warps
-        bar_all(3, ALL);
+        bar_all(kAllBar, ALL);
         const int d = channel(wq, lane);
         auto element = [&](int k) {
             const int byte = d * (int)sizeof(Bits);
@@ -374,14 +379,14 @@ struct TcKernel {
                         if (nan || minus) neg |= 1u << r;
                     }
                 }
-        bar_all(3, ALL);   // all have read
+        bar_all(kAllBar, ALL);   // all have read
         if (d >= 0 && row0 == 0)
             for (int x = 0; x < 4; ++x)
                 for (uint32_t m = bits[x]; m; m &= m - 1) {
                     Bits* e = element(32 * x + __ffs(m) - 1);
                     if (!finite(*e)) *e = 0;
                 }
-        bar_all(3, ALL);   // the list may be written again
+        bar_all(kAllBar, ALL);   // the list may be written again
     }
 
     // 8 rows of O^T, the parts summed up
@@ -412,7 +417,7 @@ struct TcKernel {
         float l[RW];
         uint32_t pos = 0, neg = 0;
         bool bad = false;
-        for (int t = 0; t < T; ++t) {
+        for (int t = 0;; ++t) {
             bad |= !wait_warp(sb + C::MFULL + 8 * (t % C::MD), (t / C::MD) & 1);
             const Meta mt = *meta(t);
             const bool first = mt.flags & kFirst, edge = mt.flags & kEdge;
@@ -439,8 +444,8 @@ struct TcKernel {
             const int j = mt.j0 + key;
             float s[RW];
             if (rows > 0) {
-                if constexpr (RW == 32) tmem_ld32(tS, s);
-                else tmem_ld16(tS, s);
+                if constexpr (RW == 16) tmem_ld16(tS, s);
+                else tmem_ld8(tS, s);
                 tmem_wait_ld();
             }
             uint32_t up = 0;   // counted without branches
@@ -567,7 +572,7 @@ struct TcKernel {
                 if constexpr (F8) {
 #pragma unroll
                     for (int y = 0; y < 3; ++y)
-                        *reinterpret_cast<uint2*>(at + y * (N / 16) * (TOK * 16) + c % 16) = make_uint2(part[y][0], part[y][1]);
+                        *reinterpret_cast<uint2*>(at + y * (N / 16) * (TOK * 16) + (row0 + c) % 16) = make_uint2(part[y][0], part[y][1]);
                 } else {
                     *reinterpret_cast<uint4*>(at) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                 }
@@ -593,22 +598,23 @@ struct TcKernel {
 
             // the item's end here: the sums while the last product runs, then the outputs
             float* to = P.partial + (int64_t)mt.part * (N * (D + 2)) + row0;   // of a split item
-            // sums over the warp's keys: lane i of the first 16 ends with row 16 x + i
+            // sums over the warp's keys: lane i of the first RW ends with row i
+            if (rows > 0) {
+                float v[RW];
 #pragma unroll
-            for (int x = 0; x < RW / 16; ++x) {
-                if (16 * x >= rows) break;
-                float v[16];
+                for (int i = 0; i < RW; ++i) {
+                    v[i] = l[i] + __shfl_xor_sync(0xffffffffu, l[i], 16);
+                    if (RW == 8) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 8);
+                }
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = l[16 * x + i] + __shfl_xor_sync(0xffffffffu, l[16 * x + i], 16);
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1)
+                for (int o = RW / 2; o > 0; o >>= 1)
 #pragma unroll
                     for (int i = 0; i < o; ++i) {
                         const bool hi = lane & o;
                         const float give = hi ? v[i] : v[i + o], keep = hi ? v[i + o] : v[i];
                         v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
                     }
-                if (lane < 16) wred[wq * N + 16 * x + lane] = v[0];
+                if (lane < RW) wred[wq * N + lane] = v[0];
             }
             bar_all(bar, 128);
             float sum = 0.f, top = 0.f;
@@ -676,6 +682,7 @@ struct TcKernel {
                     P.lse[(mt.t0 + tk) * P.Hq + mt.h * P.group + (ir - tk * P.group)] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
                 }
             }
+            if (mt.flags & kEnd) break;
         }
         if (bad) fail();
     }
@@ -686,39 +693,43 @@ struct TcKernel {
         W w(P);
         w.template find<C::THREADS>(reinterpret_cast<int64_t*>(sm + C::RING));
         kda_grid_launch_next();
-        T = (int)(w.end - w.begin);
-        if (T == 0) {
-            if (tid == 0) P.split[blockIdx.x].last = -1;
-            return;
-        }
+        Fetch<C, N> f{P, lane, {}};
         if (warp == 0) sm100::tmem_alloc(sb + C::TMEM, C::TCOLS);
-        if (tid == 32) {
-            for (int i = 0; i < C::STG; ++i) {
-                sm100::mbar_init(sb + C::FULL + 8 * i, 1);
-                sm100::mbar_init(sb + C::EMPTY + 8 * i, 1);
-                sm100::mbar_init(sb + C::QRAW + 8 * i, 1);
-                sm100::mbar_init(sb + C::QFULL + 8 * i, F8 ? C::LW : 1);
+        if (warp == C::SW) {
+            if (lane == 0) {
+                for (int i = 0; i < C::STG; ++i) {
+                    sm100::mbar_init(sb + C::FULL + 8 * i, 1);
+                    sm100::mbar_init(sb + C::EMPTY + 8 * i, 1);
+                    sm100::mbar_init(sb + C::QRAW + 8 * i, 1);
+                    sm100::mbar_init(sb + C::QFULL + 8 * i, F8 ? C::LW : 1);
+                }
+                for (int i = 0; i < C::MD; ++i) sm100::mbar_init(sb + C::MFULL + 8 * i, 1);
+                for (int i = 0; i < 2; ++i) {
+                    sm100::mbar_init(sb + C::SFULL + 8 * i, 1);
+                    sm100::mbar_init(sb + C::SFREE + 8 * i, C::SW);
+                    sm100::mbar_init(sb + C::PVDONE + 8 * i, 1);
+                    sm100::mbar_init(sb + C::OFREE + 8 * i, C::SW);
+                }
+                sm100::mbar_init(sb + C::PFULL, C::SW);
+                sm100::mbar_init(sb + C::FIN, 1);
+                sm100::fence_mbar_init();
             }
-            for (int i = 0; i < C::MD; ++i) sm100::mbar_init(sb + C::MFULL + 8 * i, 1);
-            for (int i = 0; i < 2; ++i) {
-                sm100::mbar_init(sb + C::SFULL + 8 * i, 1);
-                sm100::mbar_init(sb + C::SFREE + 8 * i, C::SW);
-                sm100::mbar_init(sb + C::PVDONE + 8 * i, 1);
-                sm100::mbar_init(sb + C::OFREE + 8 * i, C::SW);
-            }
-            sm100::mbar_init(sb + C::PFULL, C::SW);
-            sm100::mbar_init(sb + C::FIN, 1);
-            sm100::fence_mbar_init();
-            *reinterpret_cast<volatile uint32_t*>(sm + C::ABORT) = 0;
+            const bool any = f.begin(w);
+            if (lane == 0) *reinterpret_cast<volatile uint32_t*>(sm + C::ABORT) = 0;
+            if (lane == 0) *reinterpret_cast<volatile uint32_t*>(sm + C::BITS) = any;
         }
         sm100::tc_fence_before();
         __syncthreads();
         sm100::tc_fence_after();
         const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + C::TMEM);
-        if (warp < C::SW) {
+        const bool any = *reinterpret_cast<volatile uint32_t*>(sm + C::BITS);
+        __syncthreads();   // the word is sanitize's
+        if (!any) {
+            // nothing to do here
+        } else if (warp < C::SW) {
             softmax(tmem, warp, lane);
         } else if (warp == C::SW) {
-            fetcher(w, lane);
+            fetcher(f, w);
         } else if (warp == C::SW + 1) {
             issuer(tmem);
         } else {
@@ -727,7 +738,6 @@ struct TcKernel {
         sm100::tc_fence_before();
         __syncthreads();
         sm100::tc_fence_after();
-        if (tid == 0 && aborted()) drain();
         __syncwarp();
         if (warp == 0) sm100::tmem_dealloc(tmem, C::TCOLS);
     }
@@ -736,7 +746,7 @@ struct TcKernel {
 template <int D, typename TC, int N>
 __global__ void __launch_bounds__(Tc<D, TC, N>::THREADS, 1) attend_tc_kernel(const __grid_constant__ Params P) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    TcKernel<D, TC, N> k{P, smem, sm100::smem_u32(smem), 0};
+    TcKernel<D, TC, N> k{P, smem, sm100::smem_u32(smem)};
     k.run();
 }
 
