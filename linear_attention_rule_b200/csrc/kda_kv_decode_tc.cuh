@@ -20,7 +20,7 @@
 // side in N, which costs nothing while the long operand bounds the product:
 //   a query row is scaled by a power of two to a largest element in [2^7, 2^8); q = q1 + q2 / 16
 //     holds bf16's 8 bits, down to 2^-22 of the row's largest;
-//   a weight, in fp16 (2^-11), is p1 + p2 / 16 + p3 / 256 exactly, down to 2^-26 of the row's largest.
+//   a weight, in fp16 (2^-11), is p1 + p2 / 16 + p3 / 256 exactly, down to 2^-25 of the row's largest.
 // The products are exact and summed in fp32: 2^-25 of the sum of magnitudes over 128 products.  The
 // other way, turning the cache's tiles into fp16 images, took eight warps 1,900 cycles an operand and
 // four times the shared-memory traffic: 151 us for 75,800 keys of 8 heads.
@@ -43,9 +43,9 @@ struct Tc {
     static constexpr int QP = F8 ? 2 : 1, PP = F8 ? 3 : 1;                    // parts of queries and weights
     // The running maximum follows the scores only when they exceed it by SLACK (in units of log 2):
     // until then acc is not rescaled.  Weights are 2^(s - m + BASE): up to 2^8, which fp32 sums and bf16
-    // weights hold as well as 1; with e4m3 parts from 2^8 (the smallest parts then lie furthest below
-    // the largest weight) to 430 (e4m3 ends at 448).
-    static constexpr float BASE = F8 ? 8.f : 0.f, SLACK = F8 ? 0.75f : 8.f;
+    // weights hold as well as 1; with e4m3 parts from 2^7 (the smallest parts then lie far below the
+    // largest weight) to 2^8.75 (e4m3 ends at 448).
+    static constexpr float BASE = F8 ? 7.f : 0.f, SLACK = F8 ? 1.75f : 8.f;
     static constexpr int ROWB = D * (int)sizeof(TC);                   // a cache row
     // an operand image: BLKS blocks of rows of BROWB bytes, swizzled over those
     static constexpr int BROWB = ROWB < 128 ? ROWB : 128, BLKS = ROWB / BROWB, BLOCK = TOK * BROWB, RAW = TOK * ROWB;
@@ -63,7 +63,7 @@ struct Tc {
     // A stage is free when its tile is done; queries need one slot per stage, meta is read a little longer.
     static constexpr int metas(int stg) { return stg + 2; }
     static constexpr int misc(int stg) {
-        return metas(stg) * 64 + metas(stg) * 16 + stg * N * 4 + N * 8 + N * 8 + 4 * N * 4 + N * 4 + 8 * (4 * stg + metas(stg) + 12) + 32 + stg * 4;
+        return metas(stg) * 64 + metas(stg) * 16 + stg * N * 4 + N * 8 + N * 8 + 4 * N * 4 + N * 4 + 8 * (4 * stg + metas(stg) + 13) + 16 + 4 * SW + stg * 4;
     }
     static constexpr int total(int stg) { return stg * (STAGE + QB) + PB + misc(stg); }
     static constexpr int most(int stg) { return stg > 2 && total(stg) > kMaxSmem ? most(stg - 1) : stg; }
@@ -79,7 +79,8 @@ struct Tc {
     // barriers
     static constexpr int FULL = BAR, EMPTY = FULL + 8 * STG, QRAW = EMPTY + 8 * STG, QFULL = QRAW + 8 * QS, MFULL = QFULL + 8 * QS,
                          SFULL = MFULL + 8 * MD, SFREE = SFULL + 16, PFULL = SFREE + 16, PVDONE = PFULL + 8, OFREE = PVDONE + 16,
-                         FIN = OFREE + 16, TMEM = FIN + 8, ABORT = TMEM + 4, BITS = ABORT + 4, QLAST = BITS + 16;
+                         FIN = OFREE + 16, LOOKED = FIN + 8, TMEM = LOOKED + 8, ABORT = TMEM + 4, ANY = ABORT + 4, BITS = ANY + 4,
+                         QLAST = BITS + 4 * SW;
     static_assert(QLAST + QS * 4 <= BYTES, "misc");
     // byte offset of 16-byte chunk ch of a row of an image
     static __device__ __forceinline__ uint32_t chunk(uint32_t row, uint32_t ch) {
@@ -141,8 +142,8 @@ struct TcKernel {
     typedef Walk<C::TOK, N> W;
     static constexpr bool F8 = C::F8;
     static constexpr int TOK = C::TOK;
-    // named barriers: 1 .. of the groups of softmax warps, of all of them, of the splitting warps
-    static constexpr uint32_t kAllBar = 1 + C::SW / 4, kSplitBar = 2 + C::SW / 4;
+    // named barriers: 1 .. of the groups of softmax warps, then of the splitting warps
+    static constexpr uint32_t kSplitBar = 1 + C::SW / 4;
 
     const Params& P;
     uint8_t* sm;
@@ -340,9 +341,11 @@ struct TcKernel {
     // Keys that some tokens see and some do not take part in the product for all (with weight 0
     // for those that do not see them), which a NaN or infinity among their values would break: such
     // elements are taken out of the image, and the channel's rows that see them noted in pos / neg.
-    // All softmax warps.
-    __device__ __forceinline__ void sanitize(const Meta& mt, int t, bool ok, int wq, int lane, int row0, uint32_t& pos, uint32_t& neg) {
-        constexpr uint32_t ALL = 32 * C::SW;
+    // Each group of four warps looks for itself; the first takes the elements out when all have looked.
+    // False when that wait ran out.
+    __device__ __forceinline__ bool sanitize(const Meta& mt, int t, bool ok, int w, int lane, uint32_t& events, uint32_t& pos, uint32_t& neg) {
+        const int wq = w & 3, row0 = (w >> 2) * C::RW;
+        const uint32_t bar = 1 + (w >> 2);
         uint8_t* v = v_image(t);
         const int key = 32 * wq + lane, j = mt.j0 + key;
         uint32_t bad = 0;
@@ -356,11 +359,11 @@ struct TcKernel {
                     bad |= F8 ? ((a[x] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u : ((a[x] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
             }
         }
-        if (!bar_any(kAllBar, bad != 0, ALL)) return;
-        volatile uint32_t* bits = reinterpret_cast<volatile uint32_t*>(sm + C::BITS);
+        if (!bar_any(bar, bad != 0, 128)) return true;
+        volatile uint32_t* bits = reinterpret_cast<volatile uint32_t*>(sm + C::BITS) + (w & ~3);
         const uint32_t mine = __ballot_sync(0xffffffffu, bad != 0);
-        if (lane == 0) bits[wq] = mine;   // the same of both groups of warps
-        bar_all(kAllBar, ALL);
+        if (lane == 0) bits[wq] = mine;
+        bar_all(bar, 128);
         const int d = channel(wq, lane);
         auto element = [&](int k) {
             const int byte = d * (int)sizeof(Bits);
@@ -379,14 +382,18 @@ struct TcKernel {
                         if (nan || minus) neg |= 1u << r;
                     }
                 }
-        bar_all(kAllBar, ALL);   // all have read
-        if (d >= 0 && row0 == 0)
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(sb + C::LOOKED);
+        const uint32_t phase = events++ & 1;
+        if (row0) return true;
+        if (!wait_warp(sb + C::LOOKED, phase)) return false;
+        if (d >= 0)
             for (int x = 0; x < 4; ++x)
                 for (uint32_t m = bits[x]; m; m &= m - 1) {
                     Bits* e = element(32 * x + __ffs(m) - 1);
                     if (!finite(*e)) *e = 0;
                 }
-        bar_all(kAllBar, ALL);   // the list may be written again
+        return true;
     }
 
     // 8 rows of O^T, the parts summed up
@@ -415,7 +422,7 @@ struct TcKernel {
         float* frow = reinterpret_cast<float*>(sm + C::FROW) + row0;
         const float cap2 = P.softcap * kLog2e;
         float l[RW];
-        uint32_t pos = 0, neg = 0;
+        uint32_t pos = 0, neg = 0, events = 0;
         bool bad = false;
         for (int t = 0;; ++t) {
             bad |= !wait_warp(sb + C::MFULL + 8 * (t % C::MD), (t / C::MD) & 1);
@@ -435,8 +442,8 @@ struct TcKernel {
                 for (int r = 0; r < RW; ++r) l[r] = 0.f;
                 pos = neg = 0;
             }
+            if (first) bar_all(bar, 128);
             bad |= !wait_warp(sb + C::SFULL + 8 * (t & 1), (t >> 1) & 1);
-            if (bar_any(bar, bad || aborted(), 128)) break;
             tc_fence_after();
             const bool ok = (reinterpret_cast<const uint32_t*>(sm + C::OKM + (t % C::MD) * 16)[wq] >> lane) & 1;
             const bool mask = edge || !__all_sync(0xffffffffu, ok);
@@ -500,7 +507,8 @@ struct TcKernel {
             }
             // the weights of the tile before, and O, are free
             if (t > 0) bad |= !wait_warp(sb + C::PVDONE + 8 * ((t - 1) & 1), ((t - 1) >> 1) & 1);
-            if (bar_any(bar, up != 0, 128)) {
+            if (bar_any(bar, up != 0 || bad, 128)) {
+                if (bar_any(bar, bad, 128)) break;   // a wait ran out: all stop here
                 // some row's maximum rises: the new one, and what the sums so far are worth in it
                 tc_fence_after();
                 float mine = -INFINITY;
@@ -585,7 +593,7 @@ struct TcKernel {
             if (edge && mt.nq > 1) {
                 bad |= !wait_full(t);
                 __syncwarp();
-                sanitize(mt, t, ok, wq, lane, row0, pos, neg);
+                bad |= !sanitize(mt, t, ok, w, lane, events, pos, neg);
             }
             tc_fence_before();
             fence_proxy_async_smem();
@@ -712,19 +720,18 @@ struct TcKernel {
                 }
                 sm100::mbar_init(sb + C::PFULL, C::SW);
                 sm100::mbar_init(sb + C::FIN, 1);
+                sm100::mbar_init(sb + C::LOOKED, C::SW);
                 sm100::fence_mbar_init();
             }
             const bool any = f.begin(w);
             if (lane == 0) *reinterpret_cast<volatile uint32_t*>(sm + C::ABORT) = 0;
-            if (lane == 0) *reinterpret_cast<volatile uint32_t*>(sm + C::BITS) = any;
+            if (lane == 0) *reinterpret_cast<volatile uint32_t*>(sm + C::ANY) = any;
         }
         sm100::tc_fence_before();
         __syncthreads();
         sm100::tc_fence_after();
         const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + C::TMEM);
-        const bool any = *reinterpret_cast<volatile uint32_t*>(sm + C::BITS);
-        __syncthreads();   // the word is sanitize's
-        if (!any) {
+        if (!*reinterpret_cast<volatile uint32_t*>(sm + C::ANY)) {
             // nothing to do here
         } else if (warp < C::SW) {
             softmax(tmem, warp, lane);
