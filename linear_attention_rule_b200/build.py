@@ -1,4 +1,5 @@
-"""Build libkda.so in-tree for sm_100a with nvcc (no JIT cache, no torch extension)."""
+"""Build in-tree: libkda.so for sm_100a with nvcc (no JIT cache, no torch in it), and kda_native.so, the
+binding's argument marshalling for the calls of a decode step, with the host compiler against torch."""
 from __future__ import annotations
 
 import os
@@ -10,6 +11,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libkda.so")
+NATIVE_SRC = os.path.join(PKG, "native", "kda_native.cpp")
+NATIVE = os.path.join(PKG, "kda_native.so")
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",
@@ -24,24 +27,49 @@ def sources():
         os.path.join(INCLUDE, "libkda.h")]
 
 
+def _stale(target: str, inputs) -> bool:
+    return not os.path.exists(target) or any(os.path.getmtime(s) > os.path.getmtime(target) for s in inputs)
+
+
 def needs_build() -> bool:
-    if not os.path.exists(LIB):
-        return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(s) > t for s in sources())
+    return _stale(LIB, sources())
 
 
-def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    if not force and not needs_build():
-        return LIB
-    nvcc = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
-    tmp = LIB + ".tmp.%d" % os.getpid()
-    cmd = [nvcc] + NVCC_FLAGS + (["-Xptxas", "-v"] if ptxas_info else []) + [
-        "-I", INCLUDE, "-I", CSRC, os.path.join(CSRC, "libkda.cu"), "-o", tmp]
+def _run(cmd, target: str, verbose: bool) -> None:
+    """Run a compiler that writes to a file of its own, then put that in the target's place."""
+    tmp = target + ".tmp.%d" % os.getpid()
+    cmd = cmd + ["-o", tmp]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.check_call(cmd)
-    os.replace(tmp, LIB)
+    os.replace(tmp, target)
+
+
+def build_native(force: bool = False, verbose: bool = False) -> str:
+    header = os.path.join(INCLUDE, "libkda.h")
+    if not force and not _stale(NATIVE, [NATIVE_SRC, header]):
+        return NATIVE
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    cuda = os.path.dirname(os.path.dirname(os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")))
+    includes = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(cuda, "include")] + cpp_extension.include_paths()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI)]
+    cmd += [x for d in includes for x in ("-isystem", d)] + [NATIVE_SRC]
+    cmd += [x for d in cpp_extension.library_paths() for x in ("-L" + d, "-Wl,-rpath," + d)]
+    _run(cmd + ["-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], NATIVE, verbose)
+    return NATIVE
+
+
+def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
+    if force or needs_build():
+        nvcc = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
+        _run([nvcc] + NVCC_FLAGS + (["-Xptxas", "-v"] if ptxas_info else []) + [
+            "-I", INCLUDE, "-I", CSRC, os.path.join(CSRC, "libkda.cu")], LIB, verbose)
+    build_native(force, verbose)
     return LIB
 
 

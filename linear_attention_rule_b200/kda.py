@@ -1,4 +1,5 @@
-"""Thin Python binding of libkda (ctypes).  Argument marshalling only.
+"""Thin Python binding of libkda (ctypes, and native/kda_native.cpp for the short calls of a decode
+step).  Argument marshalling only.
 
 Every function has the name of the C entry point it calls (include/libkda.h) and
 passes torch tensors' device pointers, sizes and the current CUDA stream straight
@@ -8,6 +9,8 @@ fallback: if libkda.so is missing or a call fails, a RuntimeError is raised.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 from typing import Optional
 
@@ -15,6 +18,7 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libkda.so")
+NATIVE_PATH = os.path.join(_PKG, "kda_native.so")
 
 KDA_OK = 0
 KDA_ERR_INVALID_ARG = 1
@@ -49,6 +53,7 @@ EXPORTED = ("kda_prefill", "kda_prefill_workspace_size", "kda_decode", "kda_stat
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 _lib = None
+_native_module = None
 
 
 class KdaError(RuntimeError):
@@ -123,18 +128,21 @@ def load() -> ctypes.CDLL:
     return lib
 
 
-class _KvCache(ctypes.Structure):   # kda_kv_cache
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
-                ("v_scale", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
-                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64),
-                ("table_stride", ctypes.c_int64), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
-                ("max_pages", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32),
-                ("dt", ctypes.c_int)]
-
-
-class _Rope(ctypes.Structure):   # kda_rope
-    _fields_ = [("inv_freq", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
-                ("num_axes", ctypes.c_int32), ("axis_pairs", ctypes.c_int32 * 4), ("adjacent", ctypes.c_int32)]
+def _native():
+    """The marshalling of the decode step's calls (built in-tree by linear_attention_rule_b200.build), bound to
+    the loaded library."""
+    global _native_module
+    if _native_module is None:
+        lib = load()
+        if not os.path.exists(NATIVE_PATH):
+            raise RuntimeError("kda_native.so is not built (%s); run __graft_entry__.build()" % NATIVE_PATH)
+        loader = importlib.machinery.ExtensionFileLoader("kda_native", NATIVE_PATH)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("kda_native", NATIVE_PATH, loader=loader))
+        loader.exec_module(module)
+        module.init(*(ctypes.cast(f, ctypes.c_void_p).value
+                      for f in (lib.kda_decode_pool, lib.kda_kv_append, lib.kda_kv_decode)))
+        _native_module = module
+    return _native_module
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -451,80 +459,6 @@ def _decode(fn, q, k, v, g, beta, state, out, stream):
     return out
 
 
-_CACHE_CODES = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16, torch.float8_e4m3fn: KDA_E4M3}
-
-
-def _dense(device, name, t, shape, dtype):
-    """The device pointer of one dense argument (0 for None), checked as _check does."""
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.shape != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    if t.device != device or device.type != "cuda":
-        raise ValueError("%s must be on %s (libkda takes device pointers), got %s" % (name, device, t.device))
-    return t.data_ptr()
-
-
-def _rows(device, name, t, shape, dtype):
-    """(device pointer, elements from token to token) of q, k or v [tokens, heads, D]: the head
-    and channel axes dense, the token axis free (a slice of a fused projection)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.shape != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    tokens, heads, D = shape
-    st = t.stride()
-    if tokens * heads and ((st[1] != D and heads > 1) or st[2] != 1):
-        raise ValueError("%s must be dense in its last two axes" % name)
-    if t.device != device or device.type != "cuda":
-        raise ValueError("%s must be on %s (libkda takes device pointers), got %s" % (name, device, t.device))
-    return t.data_ptr(), (st[0] if tokens > 1 else heads * D)
-
-
-class _On:
-    """The device of a call's tensors made current (when it is not), and the raw stream there:
-    `stream`, or that device's current stream."""
-
-    def __init__(self, device, stream):
-        self.guard = None
-        if torch.cuda.current_device() != device.index:
-            self.guard = torch.cuda.device(device)
-        self.device, self.stream = device, stream
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        s = self.stream
-        if s is None:
-            return torch._C._cuda_getCurrentRawStream(self.device.index)
-        if s.device != self.device:
-            self.__exit__(None, None, None)
-            raise ValueError("the stream must be on %s, got %s" % (self.device, s.device))
-        return s.cuda_stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-
-def _seqs(device, cu_seqlens, T):
-    """(pointer, number of sequences) of cu_seqlens, None meaning one token per sequence."""
-    if cu_seqlens is None:
-        return None, T
-    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
-        raise ValueError("cu_seqlens must be an int32 tensor [N+1]")
-    N = cu_seqlens.shape[0] - 1
-    return _dense(device, "cu_seqlens", cu_seqlens, (N + 1,), torch.int32), N
-
-
 def kda_decode_pool(q, k, v, g, beta, state_pool, slots_in, slots_out, out, cu_seqlens=None, in_flags: int = 0,
                     stream=None):
     """The gated delta rule over a pool of states, one or several tokens per sequence
@@ -535,54 +469,10 @@ def kda_decode_pool(q, k, v, g, beta, state_pool, slots_in, slots_out, out, cu_s
     [slots, Hv, D, D], updated; slots_in int32 [N] (-1: a fresh state); slots_out int32 [T]
     (-1: not stored); cu_seqlens int32 [N+1], or None for one token per sequence.
     """
-    lib = load()
-    dt = _dtype_code(q)
-    if q.dim() != 3 or v.dim() != 3 or state_pool.dim() != 4:
-        raise ValueError("q and v must be [T, H, D] and state_pool [slots, Hv, D, D]")
-    T, Hk, D = q.shape
-    Hv = v.shape[1]
-    dev, ty = q.device, q.dtype
-    cu, N = _seqs(dev, cu_seqlens, T)
-    pq, sq = _rows(dev, "q", q, (T, Hk, D), ty)
-    pk, sk = _rows(dev, "k", k, (T, Hk, D), ty)
-    pv, sv = _rows(dev, "v", v, (T, Hv, D), ty)
-    slots = state_pool.shape[0]
-    args = (_dense(dev, "g", g, (T, Hv) if in_flags & KDA_IN_G_SCALAR else (T, Hv, D), torch.float32),
-            _dense(dev, "beta", beta, (T, Hv), torch.float32), sq, sk, sv,
-            _dense(dev, "state_pool", state_pool, (slots, Hv, D, D), torch.float32), slots,
-            _dense(dev, "slots_in", slots_in, (N,), torch.int32),
-            _dense(dev, "slots_out", slots_out, (T,), torch.int32), cu, N, T, Hk, Hv, D, D, dt,
-            _dense(dev, "out", out, (T, Hv, D), ty), in_flags)
-    with _On(dev, stream) as raw:
-        st = lib.kda_decode_pool(pq, pk, pv, *args, raw)
+    st = _native().decode_pool(q, k, v, g, beta, state_pool, slots_in, slots_out, out, cu_seqlens, in_flags, stream)
     if st != KDA_OK:
         raise KdaError("kda_decode_pool", st)
     return out
-
-
-def _kv_cache(dev, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, N):
-    """The kda_kv_cache of k_cache, v_cache [pages, Hkv, page_size, D] (any strides, alike)."""
-    if k_cache.dim() != 4 or k_cache.dtype not in _CACHE_CODES:
-        raise ValueError("k_cache must be [pages, Hkv, page_size, D] in float32, bfloat16 or float8_e4m3fn")
-    shape, strides = k_cache.shape, k_cache.stride()
-    if v_cache.shape != shape or v_cache.dtype != k_cache.dtype or v_cache.stride() != strides:
-        raise ValueError("v_cache must have the shape, type and strides of k_cache")
-    if strides[3] != 1:
-        raise ValueError("the caches must be dense in their last axis")
-    pages, Hkv, ps, D = shape
-    if k_cache.device != dev or v_cache.device != dev or dev.type != "cuda":
-        raise ValueError("the caches must be on %s (libkda takes device pointers)" % dev)
-    if (not isinstance(block_table, torch.Tensor) or block_table.dim() != 2 or block_table.dtype != torch.int32
-            or block_table.shape[0] != N or (block_table.shape[1] > 1 and block_table.stride(1) != 1)):
-        raise ValueError("block_table must be int32 [%d, pages of a sequence], dense in its last axis" % N)
-    if block_table.device != dev:
-        raise ValueError("block_table must be on %s, got %s" % (dev, block_table.device))
-    width = block_table.shape[1]
-    return _KvCache(k_cache.data_ptr(), v_cache.data_ptr(), _dense(dev, "k_scale", k_scale, (Hkv,), torch.float32),
-                    _dense(dev, "v_scale", v_scale, (Hkv,), torch.float32), block_table.data_ptr(),
-                    _dense(dev, "seq_lens", seq_lens, (N,), torch.int32),
-                    strides[0] if pages > 1 else D, strides[1] if Hkv > 1 else D, strides[2] if ps > 1 else D,
-                    block_table.stride(0) if N > 1 else width, pages, ps, width, Hkv, D, _CACHE_CODES[k_cache.dtype])
 
 
 def kda_kv_append(k, v, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None, q=None, q_out=None,
@@ -599,47 +489,11 @@ def kda_kv_append(k, v, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None
     [axes, T] (None: places in the sequence); axis_pairs: pairs per axis.  Returns q_out,
     allocated when not given.
     """
-    lib = load()
-    dt = _dtype_code(k)
-    if k.dim() != 3:
-        raise ValueError("k must be [T, Hkv, D]")
-    T, Hkv, D = k.shape
-    dev, ty = k.device, k.dtype
-    cu, N = _seqs(dev, cu_seqlens, T)
-    pk, sk = _rows(dev, "k", k, (T, Hkv, D), ty)
-    pv, sv = _rows(dev, "v", v, (T, Hkv, D), ty)
-    cache = _kv_cache(dev, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, N)
-    if k_cache.shape[1] != Hkv or k_cache.shape[3] != D:
-        raise ValueError("the caches must hold %d heads of %d channels, got shape %s" % (Hkv, D, tuple(k_cache.shape)))
-    rope = None
-    if inv_freq is not None:
-        if inv_freq.dim() != 1:
-            raise ValueError("inv_freq must be fp32 [pairs]")
-        pairs = inv_freq.shape[0]
-        axes = 1 if positions is None or positions.dim() == 1 else positions.shape[0]
-        per = (pairs,) if axis_pairs is None and axes == 1 else tuple(axis_pairs or ())
-        if len(per) != axes or not 1 <= axes <= 4:
-            raise ValueError("axis_pairs must name the pairs of each of the %d position axes (1 to 4)" % axes)
-        rope = _Rope(_dense(dev, "inv_freq", inv_freq, (pairs,), torch.float32),
-                     _dense(dev, "positions", positions, (T,) if positions is not None and positions.dim() == 1
-                            else (axes, T), torch.int32), 2 * pairs, axes, per, 1 if adjacent else 0)
-    elif positions is not None or axis_pairs is not None:
-        raise ValueError("positions and axis_pairs go with inv_freq")
-    pq, sq, Hq = None, 0, 0
-    if q is not None:
-        if q.dim() != 3:
-            raise ValueError("q must be [T, Hq, D]")
-        Hq = q.shape[1]
-        pq, sq = _rows(dev, "q", q, (T, Hq, D), ty)
-    elif q_out is not None:
-        raise ValueError("q_out goes with q")
-    with _On(dev, stream) as raw:
-        if q is not None and q_out is None:
-            with torch.cuda.stream(stream):   # None: the current stream
-                q_out = torch.empty(T, Hq, D, dtype=ty, device=dev)
-        st = lib.kda_kv_append(pk, pv, pq, sk, sv, sq, dt, ctypes.byref(cache), cu, N, T, Hq,
-                               None if rope is None else ctypes.byref(rope),
-                               _dense(dev, "q_out", q_out, (T, Hq, D), ty), raw)
+    if q_out is None and isinstance(q, torch.Tensor):
+        with torch.cuda.stream(stream):   # None: the current stream
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    st = _native().kv_append(k, v, k_cache, v_cache, block_table, seq_lens, cu_seqlens, q, q_out, inv_freq, positions,
+                             axis_pairs, adjacent, k_scale, v_scale, stream)
     if st != KDA_OK:
         raise KdaError("kda_kv_append", st)
     return q_out
@@ -662,31 +516,15 @@ def kda_kv_decode(q, k_cache, v_cache, block_table, seq_lens, out, cu_seqlens=No
     first visible key; lse fp32 [T, Hq] or None.  The workspace is allocated with torch when
     not given.
     """
-    lib = load()
-    dt = _dtype_code(q)
-    if q.dim() != 3:
-        raise ValueError("q must be [T, Hq, D]")
-    T, Hq, D = q.shape
-    dev, ty = q.device, q.dtype
-    cu, N = _seqs(dev, cu_seqlens, T)
-    pq, sq = _rows(dev, "q", q, (T, Hq, D), ty)
-    cache = _kv_cache(dev, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, N)
-    if cache.D != D or cache.Hkv < 1 or Hq % cache.Hkv:
-        raise ValueError("the caches must hold heads of %d channels that divide %d, got shape %s"
-                         % (D, Hq, tuple(k_cache.shape)))
-    po = _dense(dev, "out", out, (T, Hq, D), ty)
-    pl = _dense(dev, "lse", lse, (T, Hq), torch.float32)
-    pa = _dense(dev, "alibi_slopes", alibi_slopes, (Hq,), torch.float32)
-    ps = _dense(dev, "kv_start", kv_start, (N,), torch.int32)
-    with _On(dev, stream) as raw:
-        if workspace is None:
-            need = int(lib.kda_kv_decode_workspace_size(N, Hq, cache.Hkv, D, max_q))
-            with torch.cuda.stream(stream):   # None: the current stream
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        ws = workspace.numel()
-        st = lib.kda_kv_decode(pq, sq, dt, ctypes.byref(cache), cu, N, T, max_q, Hq,
-                               D ** -0.5 if scale is None else scale, softcap, window, pa, ps, po, pl,
-                               _dense(dev, "workspace", workspace, (ws,), torch.uint8), ws, raw)
+    native = _native()
+    if workspace is None and isinstance(q, torch.Tensor) and isinstance(k_cache, torch.Tensor):
+        # bad shapes get none, and the call below says what is wrong with them
+        Hq, Hkv, D = (q.shape[1], k_cache.shape[1], q.shape[2]) if q.dim() == 3 and k_cache.dim() == 4 else (0, 0, 0)
+        N = q.shape[0] if cu_seqlens is None else max(cu_seqlens.numel() - 1, 0)
+        with torch.cuda.stream(stream):   # None: the current stream
+            workspace = torch.empty(kda_kv_decode_workspace_size(N, Hq, Hkv, D, max_q), dtype=torch.uint8, device=q.device)
+    st = native.kv_decode(q, k_cache, v_cache, block_table, seq_lens, out, cu_seqlens, max_q, scale, softcap, window,
+                          alibi_slopes, kv_start, lse, k_scale, v_scale, workspace, stream)
     if st != KDA_OK:
         raise KdaError("kda_kv_decode", st)
     return out
