@@ -12,7 +12,8 @@
 // line, whatever the lengths.  Its tiles go through a ring of shared-memory stages.  Items that lie within one stretch are
 // finished there; the others leave a partial triple per stretch, which the join kernel adds up.
 //
-// One warp of a CTA walks its stretch and fetches the tiles with TMA: a box is the part of a page
+// Two warps of a CTA walk its stretch and fetch the tiles with TMA (a load takes about 40 issue cycles, and
+// pages of 16 rows make 32 of a 64 KB tile): one the keys, one the values and queries.  A box is the part of a page
 // in the tile (page_size rows, or the tile), so pages may end anywhere in a tile; boxes without a
 // visible key are not fetched.  The first version fetched rows with 16-byte cp.async from four warps:
 // it kept the load/store pipe so busy (1,750 of the 3,850 cycles of a 64 KB tile) that the
@@ -320,7 +321,7 @@ struct Walk {
     }
 };
 
-// The fetching warp.  C: the kernel's layout: TOK keys a tile; operands in blocks of BLK channels,
+// A fetching warp.  C: the kernel's layout: TOK keys a tile; operands in blocks of BLK channels,
 // each a run of rows of BROWB bytes; values lie RAW bytes behind the keys.
 template <typename C, int ROWS>
 struct Fetch {
@@ -329,6 +330,7 @@ struct Fetch {
 
     const Params& P;
     int lane;
+    bool keys;       // keys and what the others need to know of a tile, or values and queries
     int page[RPL];   // of the lane's rows in the tile that is fetched next, -1 where none is needed
 
     // The lane's row x lies in a box with a visible key.
@@ -361,23 +363,24 @@ struct Fetch {
             if (ok && (r & (box - 1)) == 0) ++boxes;
             if (!ok) page[x] = -1;
         }
-        if (wrong) kda_set_status(KDA_ERR_BAD_PAGE);
-        bits <<= (lane * RPL) & 31;
+        if (wrong && keys) kda_set_status(KDA_ERR_BAD_PAGE);
+        if (keys) {
+            bits <<= (lane * RPL) & 31;
 #pragma unroll
-        for (int o = 1; o < 32 / RPL; o <<= 1) bits |= __shfl_xor_sync(0xffffffffu, bits, o);
-        if (lane % (32 / RPL) == 0) okm[lane * RPL / 32] = bits;
-        boxes = __reduce_add_sync(0xffffffffu, boxes);
-        if (lane == 0) w.fill(meta);
-        __syncwarp();
-        if (lane == 0) {
-            sm100::mbar_arrive(meta_bar);
-            const uint32_t queries = w.i == 0 ? C::QB : 0;
-            sm100::mbar_arrive_expect_tx(bar, boxes * (uint32_t)(2 * box * C::ROWB) + (qbar == bar ? queries : 0));
-            if (qbar != bar && queries) *last = !w.more;
-            if (qbar != bar && queries) sm100::mbar_arrive_expect_tx(qbar, queries);
-        }
-        __syncwarp();
-        if (w.i == 0) {
+            for (int o = 1; o < 32 / RPL; o <<= 1) bits |= __shfl_xor_sync(0xffffffffu, bits, o);
+            if (lane % (32 / RPL) == 0) okm[lane * RPL / 32] = bits;
+            boxes = __reduce_add_sync(0xffffffffu, boxes);
+            if (lane == 0) w.fill(meta);
+            __syncwarp();
+            if (lane == 0) {
+                sm100::mbar_arrive(meta_bar);
+                const uint32_t queries = w.i == 0 ? C::QB : 0;
+                sm100::mbar_arrive_expect_tx(bar, boxes * (uint32_t)(2 * box * C::ROWB) + (qbar == bar ? queries : 0));
+                if (qbar != bar && queries) *last = !w.more;
+                if (qbar != bar && queries) sm100::mbar_arrive_expect_tx(qbar, queries);
+            }
+            __syncwarp();
+        } else if (w.i == 0) {
             for (int r = lane; r < ROWS; r += 32) {
                 const int ir = w.block * ROWS + r, tok = ir / P.group, g = ir - tok * P.group;
                 // rows behind the item's: a token behind the last one, which TMA fills with zeros
@@ -387,25 +390,25 @@ struct Fetch {
                     tma3(q + b * C::QBLOCK + r * C::QROWB, &P.q_map, b * (C::D / C::QBLKS), head, token, qbar);
             }
         }
+        const CUtensorMap* map = keys ? &P.k_map : &P.v_map;
 #pragma unroll
         for (int x = 0; x < RPL; ++x) {
             const int r = lane * RPL + x;
             if (page[x] < 0 || (r & (box - 1)) != 0) continue;
             const int row = (j0 + r) & ((1 << P.c.page_shift) - 1);
-            const uint32_t dst = stage + r * C::BROWB;
+            const uint32_t dst = stage + (keys ? 0 : C::RAW) + r * C::BROWB;
 #pragma unroll
             for (int b = 0; b < C::BLKS; ++b) {
-                tma4(dst + b * C::BLOCK, &P.k_map, b * (C::D / C::BLKS), row, w.h, page[x], bar);
-                tma4(dst + C::RAW + b * C::BLOCK, &P.v_map, b * (C::D / C::BLKS), row, w.h, page[x], bar);
+                tma4(dst + b * C::BLOCK, map, b * (C::D / C::BLKS), row, w.h, page[x], bar);
             }
         }
     }
     // Finds the first tile; false if the stretch has none.
     __device__ __forceinline__ bool begin(W& w) {
-        if (lane == 0) P.split[blockIdx.x].last = -1;
+        if (keys && lane == 0) P.split[blockIdx.x].last = -1;
         w.s = seq_info<C::TOK>(P, w.n, ROWS);
         if (!w.seek()) return false;
-        if (lane == 0) w.tell_join(P.split + blockIdx.x);
+        if (keys && lane == 0) w.tell_join(P.split + blockIdx.x);
         look(w);
         return true;
     }
@@ -417,7 +420,7 @@ struct Fetch {
             if (!free(t)) return false;
             at(t);
             if (!w.next()) return true;
-            if (w.i == 0 && lane == 0) w.tell_join(P.split + blockIdx.x);
+            if (keys && w.i == 0 && lane == 0) w.tell_join(P.split + blockIdx.x);
             look(w);
         }
     }
@@ -427,58 +430,77 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
-// Adds up the partial triples of the items that lie across stretches.  CTA (w, row): the item
-// that starts in worker w's stretch and goes on; groups of D threads share its parts.
-constexpr int kJoinThreads = 256;
+// Adds up the partial triples of the items that lie across stretches.  CTA (w, y): rows 8 y .. + 7 of the
+// item that starts in worker w's stretch and goes on.  A warp has one row and, with fewer than 8 rows,
+// every 8 / rows-th part of it.
+constexpr int kJoinWarps = 8;
 
 template <int D, typename T, typename TC, int ROWS>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params P) {
-    constexpr int GROUPS = kJoinThreads / D;
-    __shared__ float wt[kWorkers], sacc[GROUPS][D], red[kJoinThreads / 32], tot[2];
-    const int tid = threadIdx.x, lane = tid & 31, lr = blockIdx.y, w0 = blockIdx.x;
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ Params P) {
+    constexpr int E = D / 32;
+    __shared__ float sm[kJoinWarps], sl[kJoinWarps], sacc[kJoinWarps][D];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, w0 = blockIdx.x;
     kda_grid_wait();
     const Split s = P.split[w0];
-    const int r = s.block * ROWS + lr, parts = s.last - w0 + 1;
-    if (s.last < 0 || r >= s.nq * P.group) return;
+    const int here = min(s.nq * P.group - s.block * ROWS, ROWS) - kJoinWarps * (int)blockIdx.y;   // rows from this CTA's first on
+    if (s.last < 0 || here <= 0) return;
+    const int rows = min(here, kJoinWarps), slices = kJoinWarps / rows, row = w % rows, slice = w / rows;
+    const int lr = kJoinWarps * blockIdx.y + row, parts = s.last - w0 + 1;
     const size_t size = (size_t)ROWS * (D + 2);
     // part x: the second slot of worker w0, then the first slots of the workers behind it
     auto part = [&](int x) { return P.partial + (x == 0 ? 2 * w0 + 1 : 2 * (w0 + x)) * size; };
-    float m = -INFINITY, l = 0.f;
-    if (tid < parts) { m = part(tid)[lr]; l = part(tid)[ROWS + lr]; }   // parts <= kWorkers < kJoinThreads
-    float top = warp_max(m);
-    if (lane == 0) red[tid >> 5] = top;
-    __syncthreads();
+    float m = -INFINITY, l = 0.f, acc[E] = {};
+    if (slice < slices) {
+        for (int x0 = slice; x0 < parts; x0 += 32 * slices) {   // 32 parts at a time: a lane looks at one's statistics
+            const int x = x0 + lane * slices;
+            const float mx = x < parts ? part(x)[lr] : -INFINITY, lx = x < parts ? part(x)[ROWS + lr] : 0.f;
+            const float top = fmaxf(m, warp_max(mx)), f = m == -INFINITY ? 0.f : ex2(m - top);
+            const float wt = mx == -INFINITY ? 0.f : ex2(mx - top);
+            float sum = lx * wt;
 #pragma unroll
-    for (int x = 0; x < kJoinThreads / 32; ++x) top = x == 0 ? red[0] : fmaxf(top, red[x]);
-    const float f = m == -INFINITY ? 0.f : ex2(m - top);
-    if (tid < parts) wt[tid] = f;
-    float sum = l * f;
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            l = l * f + sum;
+            m = top;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    __syncthreads();
-    if (lane == 0) red[tid >> 5] = sum;
-    __syncthreads();
-    if (tid == 0) {
-        float t = 0.f;
-        for (int x = 0; x < kJoinThreads / 32; ++x) t += red[x];
-        tot[0] = t;
+            for (int e = 0; e < E; ++e) acc[e] *= f;
+            const int n = min(32, (parts - x0 + slices - 1) / slices);
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) {
+                const float wi = __shfl_sync(0xffffffffu, wt, i);
+                const float* from = part(x0 + i * slices) + 2 * ROWS + lr * D + lane * E;
+                float v[E];
+                if constexpr (E == 4) {
+                    const float2 a = reinterpret_cast<const float2*>(from)[0], c = reinterpret_cast<const float2*>(from)[1];
+                    v[0] = a.x; v[1] = a.y; v[2] = c.x; v[3] = c.y;
+                } else {
+                    const float2 a = *reinterpret_cast<const float2*>(from);
+                    v[0] = a.x; v[1] = a.y;
+                }
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] += wi * v[e];
+            }
+        }
+        if (lane == 0) { sm[w] = m; sl[w] = l; }
+#pragma unroll
+        for (int e = 0; e < E; ++e) sacc[w][lane * E + e] = acc[e];
     }
-    const int d = tid % D, g = tid / D;
-    float acc = 0.f;
-#pragma unroll 8
-    for (int x = g; x < parts; x += GROUPS) acc += wt[x] * part(x)[2 * ROWS + lr * D + d];
-    sacc[g][d] = acc;
     __syncthreads();
-    const float lt = tot[0];
-    const int tok = r / P.group;
+    if (slice > 0) return;
+    for (int x = 1; x < slices; ++x) {
+        const int o = x * rows + row;
+        const float top = fmaxf(m, sm[o]), f1 = m == -INFINITY ? 0.f : ex2(m - top), f2 = sm[o] == -INFINITY ? 0.f : ex2(sm[o] - top);
+        l = l * f1 + sl[o] * f2;
+        m = top;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = acc[e] * f1 + sacc[o][lane * E + e] * f2;
+    }
+    const int r = s.block * ROWS + lr, tok = r / P.group;
     const int64_t at = (s.t0 + tok) * P.Hq + s.h * P.group + (r - tok * P.group);
-    if (g == 0) {
+    const float vs = sizeof(TC) == 1 && P.c.v_scale ? P.c.v_scale[s.h] : 1.f;
+    const float f = l == 0.f ? 0.f : vs / l;
 #pragma unroll
-        for (int x = 1; x < GROUPS; ++x) acc += sacc[x][d];
-        const float vs = sizeof(TC) == 1 && P.c.v_scale ? P.c.v_scale[s.h] : 1.f;
-        static_cast<T*>(P.out)[at * D + d] = from_f32<T>(acc * (lt == 0.f ? 0.f : vs / lt));
-    }
-    if (tid == 0 && P.lse) P.lse[at] = lt == 0.f ? -INFINITY : top * kLn2 + logf(lt);
+    for (int e = 0; e < E; ++e) static_cast<T*>(P.out)[at * D + lane * E + e] = from_f32<T>(acc[e] * f);
+    if (lane == 0 && P.lse) P.lse[at] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
 }
 
 // Query rows that a CTA takes at a time.
@@ -544,8 +566,8 @@ cudaError_t launch_pair(Kernel kern, int threads, int bytes, const Params& P, cu
     err = cudaGetLastError();
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kWorkers, (unsigned)(P.group * P.max_q < ROWS ? P.group * P.max_q : ROWS));
-    cfg.blockDim = dim3(kJoinThreads);
+    cfg.gridDim = dim3(kWorkers, (unsigned)(std::min(P.group * P.max_q, ROWS) + kJoinWarps - 1) / kJoinWarps);
+    cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -15,7 +15,7 @@ namespace attend {
 template <int D_, int R>
 struct Simt {
     static constexpr int D = D_;
-    static constexpr int TOK = 32 * 128 / D, CW = 8, THREADS = 32 * (CW + 1);
+    static constexpr int TOK = 32 * 128 / D, CW = 8, THREADS = 32 * (CW + 2);
     static constexpr int ROWB = 4 * D, RAW = TOK * ROWB, STAGE = 2 * RAW;
     // for Fetch: blocks of 32 channels, 128-byte rows
     static constexpr bool QSWIZZLED = false;
@@ -215,9 +215,9 @@ struct SimtKernel {
         W w(P);
         w.template find<C::THREADS>(reinterpret_cast<int64_t*>(sm));
         kda_grid_launch_next();
-        Fetch<C, R> f{P, lane, {}};
-        if (warp == C::CW) {
-            if (lane == 0) {
+        Fetch<C, R> f{P, lane, warp == C::CW, {}};
+        if (warp >= C::CW) {
+            if (f.keys && lane == 0) {
                 for (int i = 0; i < C::STG; ++i) {
                     sm100::mbar_init(sb + C::FULL + 8 * i, 1);
                     sm100::mbar_init(sb + C::EMPTY + 8 * i, C::CW);
@@ -226,8 +226,8 @@ struct SimtKernel {
                 sm100::fence_mbar_init();
             }
             const bool any = f.begin(w);
-            if (lane == 0) *reinterpret_cast<volatile uint32_t*>(sm + C::ABORT) = 0;
-            if (lane == 0) *reinterpret_cast<volatile uint32_t*>(sm + C::ABORT + 4) = any;
+            if (f.keys && lane == 0) *reinterpret_cast<volatile uint32_t*>(sm + C::ABORT) = 0;
+            if (f.keys && lane == 0) *reinterpret_cast<volatile uint32_t*>(sm + C::ABORT + 4) = any;
         }
         __syncthreads();
         if (!*reinterpret_cast<volatile uint32_t*>(sm + C::ABORT + 4)) return;

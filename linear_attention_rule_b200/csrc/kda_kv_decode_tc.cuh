@@ -10,7 +10,7 @@
 // running maximum is shared, and the tile that raises it by more than 2^8 is rare (kSlack).
 //
 // Warps: 4 for softmax and epilogue (TMEM lanes 32 w ..) for every 8 rows (16 of 64), which share
-// nothing but keys and values; then one that fetches tiles, one that issues the products, and
+// nothing but keys and values; then two that fetch tiles, one that issues the products, and
 // with an e4m3 cache four that split queries.  S and O are double-buffered in TMEM, so the product
 // of the next tile runs during the softmax of this one and the next item starts during the epilogue
 // of the last.  Tiles land in the operand images directly: TMA's swizzle is the images'.
@@ -39,7 +39,7 @@ struct Tc {
     static constexpr int TOK = 128;
     static constexpr int RW = N == 64 ? 16 : 8, SW = 4 * N / RW;              // rows of four softmax warps, softmax warps
     static constexpr int LW = F8 ? 4 : 0;                                     // splitting warps
-    static constexpr int THREADS = 32 * (SW + 2 + LW);
+    static constexpr int THREADS = 32 * (SW + 3 + LW);
     static constexpr int QP = F8 ? 2 : 1, PP = F8 ? 3 : 1;                    // parts of queries and weights
     // The running maximum follows the scores only when they exceed it by SLACK (in units of log 2):
     // until then acc is not rescaled.  Weights are 2^(s - m + BASE): up to 2^8, which fp32 sums and bf16
@@ -701,10 +701,10 @@ struct TcKernel {
         W w(P);
         w.template find<C::THREADS>(reinterpret_cast<int64_t*>(sm + C::RING));
         kda_grid_launch_next();
-        Fetch<C, N> f{P, lane, {}};
+        Fetch<C, N> f{P, lane, warp == C::SW, {}};
         if (warp == 0) sm100::tmem_alloc(sb + C::TMEM, C::TCOLS);
-        if (warp == C::SW) {
-            if (lane == 0) {
+        if (warp == C::SW || warp == C::SW + 1) {
+            if (f.keys && lane == 0) {
                 for (int i = 0; i < C::STG; ++i) {
                     sm100::mbar_init(sb + C::FULL + 8 * i, 1);
                     sm100::mbar_init(sb + C::EMPTY + 8 * i, 1);
@@ -724,8 +724,8 @@ struct TcKernel {
                 sm100::fence_mbar_init();
             }
             const bool any = f.begin(w);
-            if (lane == 0) *reinterpret_cast<volatile uint32_t*>(sm + C::ABORT) = 0;
-            if (lane == 0) *reinterpret_cast<volatile uint32_t*>(sm + C::ANY) = any;
+            if (f.keys && lane == 0) *reinterpret_cast<volatile uint32_t*>(sm + C::ABORT) = 0;
+            if (f.keys && lane == 0) *reinterpret_cast<volatile uint32_t*>(sm + C::ANY) = any;
         }
         sm100::tc_fence_before();
         __syncthreads();
@@ -735,12 +735,12 @@ struct TcKernel {
             // nothing to do here
         } else if (warp < C::SW) {
             softmax(tmem, warp, lane);
-        } else if (warp == C::SW) {
+        } else if (warp <= C::SW + 1) {
             fetcher(f, w);
-        } else if (warp == C::SW + 1) {
+        } else if (warp == C::SW + 2) {
             issuer(tmem);
         } else {
-            if constexpr (F8) splitter(warp - C::SW - 2, lane);
+            if constexpr (F8) splitter(warp - C::SW - 3, lane);
         }
         sm100::tc_fence_before();
         __syncthreads();
