@@ -43,6 +43,7 @@ __global__ void __launch_bounds__(D) decode_pool_kernel(const Params P) {
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int rg = lane >> 3, cg = lane & 7;
     const int n = blockIdx.x / P.Hv, h = blockIdx.x - n * P.Hv;
+    kda_grid_wait();
     int64_t t0 = n, t1 = n + 1;
     if (P.cu) {
         t0 = P.cu[n];
@@ -184,8 +185,7 @@ __global__ void __launch_bounds__(D) decode_pool_kernel(const Params P) {
 
 template <int D, typename T>
 cudaError_t launch(const Params& P, cudaStream_t stream) {
-    decode_pool_kernel<D, T><<<(unsigned)P.num_seqs * (unsigned)P.Hv, D, 0, stream>>>(P);
-    return cudaGetLastError();
+    return kda_launch_chained(decode_pool_kernel<D, T>, dim3((unsigned)P.num_seqs * (unsigned)P.Hv), D, 0, stream, P);
 }
 
 }  // namespace pool

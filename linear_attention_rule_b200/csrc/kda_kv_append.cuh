@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Params P) {
     __shared__ float scos[D / 2], ssin[D / 2];
     const int tid = threadIdx.x, lane = tid & 31;
     const int64_t t = blockIdx.x;
+    kda_grid_wait();
     const int n = find_sequence(P, t, lane);
     if (n < 0) return;
     const int64_t t0 = P.cu ? P.cu[n] : n, t1 = P.cu ? P.cu[n + 1] : n + 1;
@@ -179,8 +180,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Params P) {
 
 template <int D, typename T, typename TC>
 cudaError_t launch(const Params& P, cudaStream_t stream) {
-    append_kernel<D, T, TC><<<(unsigned)P.total, kThreads, 0, stream>>>(P);
-    return cudaGetLastError();
+    return kda_launch_chained(append_kernel<D, T, TC>, dim3((unsigned)P.total), kThreads, 0, stream, P);
 }
 
 }  // namespace append

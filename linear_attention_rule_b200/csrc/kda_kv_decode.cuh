@@ -562,19 +562,10 @@ template <int D, typename T, typename TC, int ROWS, typename Kernel>
 cudaError_t launch_pair(Kernel kern, int threads, int bytes, const Params& P, cudaStream_t stream) {
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (err != cudaSuccess) return err;
-    kern<<<kWorkers, threads, bytes, stream>>>(P);
-    err = cudaGetLastError();
+    err = kda_launch_chained(kern, dim3(kWorkers), (unsigned)threads, (size_t)bytes, stream, P);
     if (err != cudaSuccess) return err;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kWorkers, (unsigned)(std::min(P.group * P.max_q, ROWS) + kJoinWarps - 1) / kJoinWarps);
-    cfg.blockDim = dim3(32 * kJoinWarps);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<D, T, TC, ROWS>, P);
+    const dim3 grid(kWorkers, (unsigned)(std::min(P.group * P.max_q, ROWS) + kJoinWarps - 1) / kJoinWarps);
+    return kda_launch_chained(join_kernel<D, T, TC, ROWS>, grid, 32 * kJoinWarps, (size_t)0, stream, P);
 }
 
 }  // namespace attend

@@ -212,6 +212,7 @@ struct SimtKernel {
     __device__ __forceinline__ void run() {
         const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
         if (tid == 0) { prefetch_map(&P.k_map); prefetch_map(&P.v_map); prefetch_map(&P.q_map); }
+        kda_grid_wait();
         W w(P);
         w.template find<C::THREADS>(reinterpret_cast<int64_t*>(sm));
         kda_grid_launch_next();
