@@ -3,10 +3,15 @@
 //
 // Pair i of a head turns by angle = position * inv_freq[i]:
 //   y1 = x1 cos - x2 sin,  y2 = x2 cos + x1 sin.
-// Positions reach 2^31 and an fp32 angle of 2^20 is off by up to 2^-5, so the angle is
-// formed in fp64, in turns, and only its fraction of a turn is rounded to fp32.  The kernel is
-// bound by memory: every element is read once and written once, and a token's sines are
-// computed once for all of its heads.
+// Positions reach 2^31 and an fp32 angle of 2^20 is off by up to 2^-5, so the angle is formed in
+// fp64, in turns; its fraction of a turn goes to fp32 in two parts, the second of which turns
+// the first part's sine and cosine to first order.  The kernel is bound by memory: every element is read
+// once and written once.
+//
+// A warp has one token, or every 2nd or 4th part of one where there are few tokens.  Its lanes hold the
+// same channels of several heads, so that a lane's sines and cosines stay in registers; the first
+// loads are on their way before the token's sequence, page and angles are known.  With a CTA per token,
+// a table of sines in shared memory and the loads behind it, 8,550 tokens of 16 + 2 x 4 heads took 48 us.
 #pragma once
 
 #include "kda_kv_cache.cuh"
@@ -24,18 +29,21 @@ struct Params {
     void* q_out;
     const float* inv_freq;
     const int32_t* positions;
-    int32_t rot, axis_end[4], adjacent;
+    int32_t rot, axis_end[4], adjacent, parts;   // parts: warps of a token
     kv::Cache c;
 };
 
-constexpr int kThreads = 128;
+constexpr int kWarps = 4;
 
 template <typename T> struct Vec8;   // 8 consecutive elements
 template <> struct Vec8<float> {
-    static __device__ __forceinline__ void load(const float* p, float* x) {
-        const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    typedef struct { float4 a, b; } Raw;
+    static __device__ __forceinline__ Raw fetch(const float* p) {
+        return {reinterpret_cast<const float4*>(p)[0], reinterpret_cast<const float4*>(p)[1]};
+    }
+    static __device__ __forceinline__ void unpack(const Raw& r, float* x) {
+        x[0] = r.a.x; x[1] = r.a.y; x[2] = r.a.z; x[3] = r.a.w;
+        x[4] = r.b.x; x[5] = r.b.y; x[6] = r.b.z; x[7] = r.b.w;
     }
     static __device__ __forceinline__ void store(float* p, const float* x) {
         reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
@@ -43,9 +51,9 @@ template <> struct Vec8<float> {
     }
 };
 template <> struct Vec8<__nv_bfloat16> {
-    static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* x) {
-        sm100::unpack_bf16x8(*reinterpret_cast<const uint4*>(p), x);
-    }
+    typedef uint4 Raw;
+    static __device__ __forceinline__ Raw fetch(const __nv_bfloat16* p) { return *reinterpret_cast<const uint4*>(p); }
+    static __device__ __forceinline__ void unpack(const Raw& r, float* x) { sm100::unpack_bf16x8(r, x); }
     static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* x) {
         *reinterpret_cast<uint4*>(p) = sm100::pack_bf16x8(x);
     }
@@ -91,96 +99,197 @@ __device__ __forceinline__ int find_sequence(const Params& P, int64_t t, int lan
     return lo;
 }
 
-// One CTA per token.
+// x / d for the quotients that are rounded to 8 bits, r = 1 / d rounded to nearest: the product's
+// remainder is exact in one fma, and with it the quotient is the correctly rounded one (Markstein 1990).
+__device__ __forceinline__ float quotient(float x, float d, float r) {
+    const float q = x * r, better = fmaf(fmaf(-q, d, x), r, q);
+    return fabsf(q) <= 3.4e38f ? better : q;   // infinities and NaN as they are
+}
+
 template <int D, typename T, typename TC>
-__global__ void __launch_bounds__(kThreads) append_kernel(const Params P) {
-    __shared__ float scos[D / 2], ssin[D / 2];
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int64_t t = blockIdx.x;
+struct Token {
+    typedef typename Vec8<T>::Raw Raw;
+    static constexpr bool F8 = sizeof(TC) == 1;
+
+    const Params& P;
+    int64_t t;
+    int lane, part;
+    // A unit is 8 channels, or 8 and their partners half a rotation on; `width` lanes have a head's.
+    int half, units, width;
+    bool mine, two;            // this lane has a unit, and it has partners
+    int c0;                    // its first channel
+    int first, step;           // this lane's heads
+    float c[8], s[8];          // cosines and sines of its pairs
+
+    __device__ __forceinline__ Token(const Params& p, int64_t token, int ln, int pt) : P(p), t(token), lane(ln), part(pt) {
+        half = P.rot / 2;
+        const int paired = P.adjacent ? 0 : half / 8;
+        units = paired + (D - (P.adjacent ? 0 : P.rot)) / 8;
+        width = units <= 8 ? 8 : 16;
+        const int u = lane % width;
+        mine = u < units;
+        two = u < paired;
+        c0 = two || P.adjacent ? 8 * u : P.rot + 8 * (u - paired);
+        step = 32 / width * P.parts;
+        first = part * (32 / width) + lane / width;
+    }
+    // Two heads, `first` and `step` behind it, of `heads`.
+    __device__ __forceinline__ void fetch(const T* src, int h, int heads, Raw (&a)[2], Raw (&b)[2]) const {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (mine && h + i * step < heads) {
+                const T* at = src + (int64_t)(h + i * step) * D;
+                a[i] = Vec8<T>::fetch(at);
+                if (two) b[i] = Vec8<T>::fetch(at + half);
+            }
+    }
+    // Sines and cosines of the token: each lane forms those of pairs lane and lane + 32, then takes its own.
+    __device__ __forceinline__ void angles(int64_t pos) {
+        float cc[2] = {1.f, 1.f}, ss[2] = {0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) {
+            const int i = lane + 32 * x;
+            if (i < half) {
+                const int axis = (i >= P.axis_end[0]) + (i >= P.axis_end[1]) + (i >= P.axis_end[2]);
+                const double where = P.positions ? (double)P.positions[axis * P.total + t] : (double)pos;
+                double turns = where * (double)P.inv_freq[i] * 0.15915494309189533577;   // 1 / (2 pi)
+                turns -= rint(turns);
+                const float hi = (float)turns, lo = (float)(turns - (double)hi) * 6.2831853f;
+                float sn, cs;
+                sincospif(2.f * hi, &sn, &cs);
+                ss[x] = sn + cs * lo;
+                cc[x] = cs - sn * lo;
+            }
+        }
+        const int p0 = P.adjacent ? c0 / 2 : c0, n = P.adjacent ? 4 : 8;   // this lane's pairs
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (j >= n) break;
+            const int i = p0 + j;
+            const float c_lo = __shfl_sync(0xffffffffu, cc[0], i & 31), s_lo = __shfl_sync(0xffffffffu, ss[0], i & 31);
+            c[j] = c_lo;
+            s[j] = s_lo;
+            if (D > 64) {
+                const float c_hi = __shfl_sync(0xffffffffu, cc[1], i & 31), s_hi = __shfl_sync(0xffffffffu, ss[1], i & 31);
+                if (i >= 32) { c[j] = c_hi; s[j] = s_hi; }
+            }
+        }
+    }
+    __device__ __forceinline__ void turn(const Raw& a, const Raw& b, float (&x)[8], float (&y)[8]) const {
+        Vec8<T>::unpack(a, x);
+        if (two) {
+            float z[8];
+            Vec8<T>::unpack(b, z);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                y[j] = z[j] * c[j] + x[j] * s[j];
+                x[j] = x[j] * c[j] - z[j] * s[j];
+            }
+        } else if (P.adjacent && c0 < P.rot) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float e = x[2 * j], o = x[2 * j + 1];
+                x[2 * j] = e * c[j] - o * s[j];
+                x[2 * j + 1] = o * c[j] + e * s[j];
+            }
+        }
+    }
+    static __device__ __forceinline__ void put(TC* dst, float (&x)[8], const float* scales, int h) {
+        if constexpr (F8) {
+            if (scales) {
+                const float d = scales[h], r = __frcp_rn(d);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = quotient(x[j], d, r);
+            }
+        }
+        Vec8<TC>::store(dst, x);
+    }
+    __device__ __forceinline__ void queries(Raw (&a)[2], Raw (&b)[2]) const {
+        const T* src = static_cast<const T*>(P.q) + t * P.q_stride + c0;
+        T* dst = static_cast<T*>(P.q_out) + t * P.Hq * D + c0;
+        for (int h = first; h < P.Hq; h += 2 * step) {
+            if (h != first) fetch(src, h, P.Hq, a, b);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float x[8], y[8];
+                if (!mine || h + i * step >= P.Hq) continue;
+                turn(a[i], b[i], x, y);
+                T* at = dst + (int64_t)(h + i * step) * D;
+                Vec8<T>::store(at, x);
+                if (two) Vec8<T>::store(at + half, y);
+            }
+        }
+    }
+    __device__ __forceinline__ void keys(int64_t row) const {
+        const T* src = static_cast<const T*>(P.k) + t * P.k_stride + c0;
+        TC* dst = static_cast<TC*>(P.c.k) + row + c0;
+        for (int h = first; h < P.c.Hkv; h += 2 * step) {
+            Raw a[2], b[2];
+            fetch(src, h, P.c.Hkv, a, b);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float x[8], y[8];
+                const int hi = h + i * step;
+                if (!mine || hi >= P.c.Hkv) continue;
+                turn(a[i], b[i], x, y);
+                put(dst + hi * P.c.head_stride, x, P.c.k_scale, hi);
+                if (two) put(dst + hi * P.c.head_stride + half, y, P.c.k_scale, hi);
+            }
+        }
+    }
+    __device__ __forceinline__ void values(int64_t row) const {   // a copy
+        constexpr int U = D / 8;
+        const T* src = static_cast<const T*>(P.v) + t * P.v_stride;
+        TC* dst = static_cast<TC*>(P.c.v) + row;
+        const int n = P.c.Hkv * U;
+        for (int e = 32 * part + lane; e < n; e += 64 * P.parts) {
+            Raw a[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (e + i * 32 * P.parts < n) a[i] = Vec8<T>::fetch(src + (int64_t)(e + i * 32 * P.parts) * 8);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int at = e + i * 32 * P.parts, h = at / U;
+                if (at >= n) continue;
+                float x[8];
+                Vec8<T>::unpack(a[i], x);
+                put(dst + h * P.c.head_stride + 8 * (at % U), x, P.c.v_scale, h);
+            }
+        }
+    }
+};
+
+template <int D, typename T, typename TC>
+__global__ void __launch_bounds__(32 * kWarps) append_kernel(const __grid_constant__ Params P) {
+    typedef Token<D, T, TC> Tok;
+    const int lane = threadIdx.x & 31;
+    const int64_t id = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int64_t t = id / P.parts;
+    const int part = (int)(id - t * P.parts);
     kda_grid_wait();
+    if (t >= P.total) return;
+    Tok k(P, t, lane, part);
+    typename Tok::Raw a[2], b[2];
+    if (P.q) k.fetch(static_cast<const T*>(P.q) + t * P.q_stride + k.c0, k.first, P.Hq, a, b);
     const int n = find_sequence(P, t, lane);
     if (n < 0) return;
     const int64_t t0 = P.cu ? P.cu[n] : n, t1 = P.cu ? P.cu[n + 1] : n + 1;
     const int64_t pos = (int64_t)P.c.seq_lens[n] - (t1 - t0) + (t - t0);
     const int64_t row = kv::row_offset(P.c, n, pos, 0);
-    if (row < 0 && tid == 0) kda_set_status(KDA_ERR_BAD_PAGE);
-    const int half = P.rot / 2;
-    for (int i = tid; i < half; i += kThreads) {
-        int axis = 0;
-        while (axis < 3 && i >= P.axis_end[axis]) ++axis;
-        const double x = P.positions ? (double)P.positions[axis * P.total + t] : (double)pos;
-        double turns = x * (double)P.inv_freq[i] * 0.15915494309189533577;   // 1 / (2 pi)
-        turns -= rint(turns);
-        sincospif(2.f * (float)turns, &ssin[i], &scos[i]);
-    }
-    __syncthreads();
-
-    // units of work: 8 channels, or 8 and their partners half a rotation on
-    const int paired = P.adjacent ? 0 : half / 8;             // units of two vectors per head
-    const int per_rot = paired + (D - (P.adjacent ? 0 : P.rot)) / 8;
-    const int rows_rot = P.Hq + P.c.Hkv;
-    const int units = rows_rot * per_rot + P.c.Hkv * (D / 8);
-    for (int u = tid; u < units; u += kThreads) {
-        float x[8], y[8];
-        if (u >= rows_rot * per_rot) {   // values: a copy
-            const int e = u - rows_rot * per_rot, h = e / (D / 8), i = e % (D / 8);
-            if (row < 0) continue;
-            Vec8<T>::load(static_cast<const T*>(P.v) + t * P.v_stride + h * D + 8 * i, x);
-            if constexpr (sizeof(TC) == 1) {
-                const float sc = P.c.v_scale ? P.c.v_scale[h] : 1.f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] /= sc;
-            }
-            Vec8<TC>::store(static_cast<TC*>(P.c.v) + row + h * P.c.head_stride + 8 * i, x);
-            continue;
-        }
-        const int hr = u / per_rot, i = u % per_rot;
-        const bool is_q = hr < P.Hq;
-        const int h = is_q ? hr : hr - P.Hq;
-        if (!is_q && row < 0) continue;
-        const T* src = is_q ? static_cast<const T*>(P.q) + t * P.q_stride + h * D
-                            : static_cast<const T*>(P.k) + t * P.k_stride + h * D;
-        const bool two = i < paired;
-        const int c0 = two ? 8 * i : (P.adjacent ? 8 * i : P.rot + 8 * (i - paired));
-        Vec8<T>::load(src + c0, x);
-        if (two) {
-            float z[8];
-            Vec8<T>::load(src + c0 + half, z);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float c = scos[c0 + j], s = ssin[c0 + j];
-                y[j] = z[j] * c + x[j] * s;
-                x[j] = x[j] * c - z[j] * s;
-            }
-        } else if (P.adjacent && c0 < P.rot) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float c = scos[c0 / 2 + j], s = ssin[c0 / 2 + j];
-                const float a = x[2 * j], b = x[2 * j + 1];
-                x[2 * j] = a * c - b * s;
-                x[2 * j + 1] = b * c + a * s;
-            }
-        }
-        if (is_q) {
-            T* dst = static_cast<T*>(P.q_out) + (t * P.Hq + h) * D + c0;
-            Vec8<T>::store(dst, x);
-            if (two) Vec8<T>::store(dst + half, y);
-        } else {
-            if constexpr (sizeof(TC) == 1) {
-                const float sc = P.c.k_scale ? P.c.k_scale[h] : 1.f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) { x[j] /= sc; y[j] /= sc; }
-            }
-            TC* dst = static_cast<TC*>(P.c.k) + row + h * P.c.head_stride + c0;
-            Vec8<TC>::store(dst, x);
-            if (two) Vec8<TC>::store(dst + half, y);
-        }
-    }
+    if (row < 0 && lane == 0) kda_set_status(KDA_ERR_BAD_PAGE);
+    if (P.rot) k.angles(pos);
+    if (P.q) k.queries(a, b);
+    if (row < 0) return;
+    k.keys(row);
+    k.values(row);
 }
 
 template <int D, typename T, typename TC>
-cudaError_t launch(const Params& P, cudaStream_t stream) {
-    return kda_launch_chained(append_kernel<D, T, TC>, dim3((unsigned)P.total), kThreads, 0, stream, P);
+cudaError_t launch(Params& P, cudaStream_t stream) {
+    // enough warps for every SM to have 16: 64 tokens by one warp each took PENDING us, by four PENDING us
+    P.parts = P.total >= 148 * 16 ? 1 : P.total >= 148 * 8 ? 2 : 4;
+    const int64_t blocks = (P.total * P.parts + kWarps - 1) / kWarps;
+    return kda_launch_chained(append_kernel<D, T, TC>, dim3((unsigned)blocks), 32 * kWarps, 0, stream, P);
 }
 
 }  // namespace append
