@@ -260,7 +260,7 @@ struct Token {
 };
 
 template <int D, typename T, typename TC>
-__global__ void __launch_bounds__(32 * kWarps) append_kernel(const __grid_constant__ Params P) {
+__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 8 : 6) append_kernel(const __grid_constant__ Params P) {
     typedef Token<D, T, TC> Tok;
     const int lane = threadIdx.x & 31;
     const int64_t id = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
