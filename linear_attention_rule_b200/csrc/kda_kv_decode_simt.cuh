@@ -2,9 +2,10 @@
 // product in three tf32 parts would need every key and value split on the way.  With up to 8
 // query rows a CTA's 36 TFMA/s / 148 keep up with its share of the memory bandwidth.
 //
-// A tile is 32 KB of keys and values.  The 8 consumer warps take it together, in three steps
-// between barriers: scores (a thread has 16 channels of one key, summed up over 4 or 8 lanes),
-// weights (warp r has row r), values (a thread has one channel and 16 keys).
+// A tile is 32 KB of keys and values.  The 8 consumer warps take it together, with one barrier: scores
+// (a thread has 16 channels of one key, summed up over 4 or 8 lanes) before it, values (a thread has one
+// channel and 16 keys) behind it.  The weights in between are formed by every warp for itself: with
+// a warp per row and another barrier a tile took half as long again.
 #pragma once
 
 #include "kda_kv_decode.cuh"
@@ -20,13 +21,13 @@ struct Simt {
     // for Fetch: blocks of 32 channels, 128-byte rows
     static constexpr bool QSWIZZLED = false;
     static constexpr int BLKS = D / 32, BROWB = 128, BLOCK = TOK * 128, QBLKS = 1, QROWB = ROWB, QBLOCK = 0;
-    static constexpr int STG = 6, QS = STG, MD = STG + 2;
+    static constexpr int STG = R <= 2 ? 6 : 5, QS = STG, MD = STG + 2;
     static constexpr int PARTS = 32 * CW / TOK, KPW = 32 / PARTS;    // lanes of a key, keys of a warp
     static constexpr int GROUPS = 32 * CW / D;                       // threads of a channel, 16 keys each
     static constexpr int QB = R * D * 4;
-    static constexpr int Q = STG * STAGE, SC = Q + QS * QB, RED = SC + 2 * R * TOK * 4;
-    static constexpr int META = RED + R * D * 4, OKM = META + MD * 64, FROW = OKM + MD * 16, ML = FROW + 2 * R * 4, FULL = ML + 2 * R * 4,
-                         EMPTY = FULL + 8 * STG, MFULL = EMPTY + 8 * STG, ABORT = MFULL + 8 * MD, BYTES = ABORT + 16;
+    static constexpr int Q = STG * STAGE, SC = Q + QS * QB, PW = SC + 2 * R * TOK * 4, RED = PW + CW * R * TOK * 4, META = RED + R * D * 4,
+                         OKM = META + MD * 64, FULL = OKM + MD * 16, EMPTY = FULL + 8 * STG, MFULL = EMPTY + 8 * STG,
+                         ABORT = MFULL + 8 * MD, BYTES = ABORT + 16;
     static_assert(BYTES <= kMaxSmem && META % 16 == 0 && FULL % 8 == 0, "shared memory of a CTA");
 };
 
@@ -76,11 +77,11 @@ struct SimtKernel {
         // eight lanes read 128 bytes without a bank twice: with 4 lanes a key, of keys 4 apart
         const int key = w * C::KPW + (C::PARTS == 4 ? (gr >> 1) | ((gr & 1) << 2) : gr);
         const int d = tid % D, kg = tid / D;
-        float acc[R], m = -INFINITY, l = 0.f;   // m, l: of row w
+        float* pw = reinterpret_cast<float*>(sm + C::PW) + w * R * TOK;   // the warp's copy of the weights
+        float acc[R], m[R], l[R], slope[R];   // l: this lane's keys
         bool bad = false;
         for (int t = 0;; ++t) {
             bad |= !wait_warp(sb + C::FULL + 8 * (t % C::STG), (t / C::STG) & 1);
-            if (bar_any(1, bad || aborted(), NT)) break;
             const Meta mt = *meta(t);
             const uint32_t* okm = reinterpret_cast<const uint32_t*>(sm + C::OKM + (t % C::MD) * 16);
             bool all = true;   // all keys there
@@ -91,95 +92,94 @@ struct SimtKernel {
             const uint8_t* v = k + C::RAW;
             const float* q = reinterpret_cast<const float*>(sm + C::Q + (mt.item % C::QS) * C::QB);
             float* sc = reinterpret_cast<float*>(sm + C::SC) + (t & 1) * R * TOK;
-            float* frow = reinterpret_cast<float*>(sm + C::FROW) + (t & 1) * R;
             if (mt.flags & kFirst) {
 #pragma unroll
-                for (int r = 0; r < R; ++r) acc[r] = 0.f;
-                m = -INFINITY;
-                l = 0.f;
+                for (int r = 0; r < R; ++r) {
+                    acc[r] = 0.f;
+                    m[r] = -INFINITY;
+                    l[r] = 0.f;
+                    slope[r] = P.slopes && r < mt.rows ? P.slopes[mt.h * P.group + (mt.block * R + r) % P.group] * kLog2e : 0.f;
+                }
             }
             {   // scores, in units of log 2; -infinity where the row does not see the key
                 float4 kk[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    kk[i] = *reinterpret_cast<const float4*>(k + chunk(key, i * C::PARTS + part));
+                for (int i = 0; i < 4; ++i) kk[i] = *reinterpret_cast<const float4*>(k + chunk(key, i * C::PARTS + part));
                 const int j = mt.j0 + key;
                 const bool ok = (okm[key >> 5] >> (key & 31)) & 1;
+                int tok = mt.tok0, left = mt.left0;
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     if (r >= mt.rows) break;
-                    float x = 0.f;
+                    float x[4];   // four short chains
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float4 a = *reinterpret_cast<const float4*>(q + r * D + (i * C::PARTS + part) * 4);
-                        x += a.x * kk[i].x + a.y * kk[i].y + a.z * kk[i].z + a.w * kk[i].w;
+                        x[i] = a.x * kk[i].x + a.y * kk[i].y + a.z * kk[i].z + a.w * kk[i].w;
                     }
+                    float y = (x[0] + x[1]) + (x[2] + x[3]);
 #pragma unroll
-                    for (int o = 1; o < C::PARTS; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+                    for (int o = 1; o < C::PARTS; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+                    const int p = mt.pos0 + tok;
                     if (part == r % C::PARTS) {
-                        const int ir = mt.block * R + r, tok = ir / P.group, p = mt.pos0 + tok;
-                        x *= P.scale;
-                        if (P.softcap > 0.f) x = P.softcap * tanhf(x / P.softcap);
-                        x *= kLog2e;
-                        if (P.slopes) x += P.slopes[mt.h * P.group + (ir - tok * P.group)] * kLog2e * (float)(j - p);
-                        if (!ok || (edge && (j > p || j < first_key(P, mt.start, p)))) x = -INFINITY;
-                        sc[r * TOK + key] = x;
+                        y *= P.scale;
+                        if (P.softcap > 0.f) y = P.softcap * tanhf(y / P.softcap);
+                        y = y * kLog2e + slope[r] * (float)(j - p);
+                        if (!ok || (edge && (j > p || j < first_key(P, mt.start, p)))) y = -INFINITY;
+                        sc[r * TOK + key] = y;
                     }
+                    if (--left == 0) { ++tok; left = P.group; }
                 }
             }
-            bar_all(1, NT);
-            if (w < mt.rows) {
+            if (bar_any(1, bad || aborted(), NT)) break;
+            float f[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (r >= mt.rows) break;
                 float x[TOK / 32], top = -INFINITY;
 #pragma unroll
                 for (int i = 0; i < TOK / 32; ++i) {
-                    x[i] = sc[w * TOK + 32 * i + lane];
+                    x[i] = sc[r * TOK + 32 * i + lane];
                     top = fmaxf(top, x[i]);
                 }
-                top = fmaxf(m, warp_max(top));
-                const float f = m == -INFINITY ? 0.f : ex2(m - top), ms = top == -INFINITY ? 0.f : top;
-                m = top;
-                l *= f;
+                top = fmaxf(m[r], warp_max(top));
+                f[r] = m[r] == -INFINITY ? 0.f : ex2(m[r] - top);
+                const float ms = top == -INFINITY ? 0.f : top;
+                m[r] = top;
+                l[r] *= f[r];
 #pragma unroll
                 for (int i = 0; i < TOK / 32; ++i) {
                     const float p = ex2(x[i] - ms);
-                    l += p;
-                    sc[w * TOK + 32 * i + lane] = x[i] == -INFINITY ? -0.f : p;   // -0: takes nothing of the value
+                    l[r] += p;
+                    pw[r * TOK + 32 * i + lane] = x[i] == -INFINITY ? -0.f : p;   // -0: takes nothing of the value
                 }
-                if (lane == 0) frow[w] = f;
             }
-            bar_all(1, NT);
+            __syncwarp();
             {
                 float vv[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int kx = kg * 16 + i;
-                    vv[i] = *reinterpret_cast<const float*>(v + chunk(kx, d >> 2) + (d & 3) * 4);
-                }
+                for (int i = 0; i < 16; ++i) vv[i] = *reinterpret_cast<const float*>(v + chunk(kg * 16 + i, d >> 2) + (d & 3) * 4);
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     if (r >= mt.rows) break;
-                    float a = acc[r] * frow[r];
+                    float a[4] = {acc[r] * f[r], 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float4 p = *reinterpret_cast<const float4*>(sc + r * TOK + kg * 16 + 4 * i);
+                        const float4 p = *reinterpret_cast<const float4*>(pw + r * TOK + kg * 16 + 4 * i);
                         const float pp[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             // a row that does not see the key takes nothing of its value, be it NaN
-                            if (!edge || __float_as_uint(pp[e]) != 0x80000000u) a += pp[e] * vv[4 * i + e];
+                            if (!edge || __float_as_uint(pp[e]) != 0x80000000u) a[i] += pp[e] * vv[4 * i + e];
                         }
                     }
-                    acc[r] = a;
+                    acc[r] = (a[0] + a[1]) + (a[2] + a[3]);
                 }
             }
             __syncwarp();
             if (lane == 0) sm100::mbar_arrive(sb + C::EMPTY + 8 * (t % C::STG));
             if (mt.flags & kLast) {
                 float* red = reinterpret_cast<float*>(sm + C::RED);
-                float* ml = reinterpret_cast<float*>(sm + C::ML);
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-                if (w < R && lane == 0) { ml[w] = m; ml[R + w] = l; }
 #pragma unroll
                 for (int g = 0; g < C::GROUPS; ++g) {   // the groups add up their keys in turn
                     if (kg == g) {
@@ -188,19 +188,23 @@ struct SimtKernel {
                     }
                     bar_all(1, NT);
                 }
-                float* to = P.partial + (int64_t)mt.part * (R * (D + 2));
-                for (int x = tid; x < mt.rows * D; x += NT) {
-                    const int r = x / D, c = x % D;
-                    const float a = red[r * D + c];
-                    const float sum = ml[R + r];
+                // a warp writes a row, and knows its statistics itself
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    if (r >= mt.rows || w != r) continue;
+                    float sum = l[r];
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                     if (mt.part < 0) {
                         const int ir = mt.block * R + r, tok = ir / P.group;
                         const int64_t at = (mt.t0 + tok) * P.Hq + mt.h * P.group + (ir - tok * P.group);
-                        static_cast<float*>(P.out)[at * D + c] = sum == 0.f ? 0.f : a / sum;
-                        if (P.lse && c == 0) P.lse[at] = sum == 0.f ? -INFINITY : ml[r] * kLn2 + logf(sum);
+                        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                        for (int c = lane; c < D; c += 32) static_cast<float*>(P.out)[at * D + c] = red[r * D + c] * inv;
+                        if (P.lse && lane == 0) P.lse[at] = sum == 0.f ? -INFINITY : m[r] * kLn2 + logf(sum);
                     } else {
-                        to[2 * R + x] = a;
-                        if (c == 0) { to[r] = ml[r]; to[R + r] = sum; }
+                        float* to = P.partial + (int64_t)mt.part * (R * (D + 2));
+                        for (int c = lane; c < D; c += 32) to[2 * R + r * D + c] = red[r * D + c];
+                        if (lane == 0) { to[r] = m[r]; to[R + r] = sum; }
                     }
                 }
                 if (mt.flags & kEnd) break;
