@@ -433,7 +433,7 @@ struct TcKernel {
                 if constexpr (F8) bad |= !wait_warp(sb + C::QFULL + 8 * (mt.item % C::QS), (mt.item / C::QS) & 1);
                 if (tid < RW) {
                     mrow[tid] = make_float2(-INFINITY, 0.f);
-                    float f = P.scale * (P.softcap > 0.f ? 2.f * kLog2e / P.softcap : kLog2e), slope = 0.f;
+                    float f = P.scale * (P.softcap > 0.f ? 1.f / P.softcap : kLog2e), slope = 0.f;
                     if (F8) f *= (P.c.k_scale ? P.c.k_scale[mt.h] : 1.f) * reinterpret_cast<const float*>(sm + C::QF)[(mt.item % C::QS) * N + row0 + tid];
                     if (P.slopes && tid < rows) slope = P.slopes[mt.h * P.group + (mt.block * N + row0 + tid) % P.group] * kLog2e;
                     info[tid] = make_float2(f, slope);   // scale of the raw products, bias per key
@@ -483,10 +483,24 @@ struct TcKernel {
                     top[i + 1] = m.z;
                 }
                 if (P.softcap > 0.f) {
-                    // cap tanh(x / cap) = cap (1 - 2 / (1 + e^{2 x / cap})): off by up to 2^-21 cap, far below the
-                    // weights' own rounding
+                    // tanh y by its Taylor series up to y^9 where |y| <= 1/4 (the next term is below 2^-26 of it: most
+                    // scores lie far below their cap, and no ex2 or rcp is spent on them), 1 - 2 / (1 + e^{2 y}) beyond
+                    float big = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) s[c + i] = cap2 - 2.f * cap2 * rcp(1.f + ex2(s[c + i] * in[i].x));
+                    for (int i = 0; i < 8; ++i) {
+                        const float y = s[c + i] * in[i].x, z = y * y;
+                        const float tail = z * (-1.f / 3 + z * (2.f / 15 + z * (-17.f / 315 + z * (62.f / 2835))));
+                        big = fmaxf(big, fabsf(y));
+                        s[c + i] = fabsf(y) > 0.25f ? y : cap2 * (y + y * tail);
+                        in[i].x = y;
+                    }
+                    if (__any_sync(0xffffffffu, big > 0.25f)) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float y = in[i].x;
+                            if (fabsf(y) > 0.25f) s[c + i] = cap2 - 2.f * cap2 * rcp(1.f + ex2(y * (2.f * kLog2e)));
+                        }
+                    }
                 } else {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) s[c + i] *= in[i].x;
