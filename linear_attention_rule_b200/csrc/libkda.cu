@@ -477,6 +477,7 @@ kda_status kda_kv_decode(const void* q, int64_t q_stride, kda_dtype dt, const kd
         !(softcap - softcap == 0.f))
         return KDA_ERR_INVALID_ARG;
     if (max_q > kMaxQ || Hq > 65535 || (int64_t)num_seqs * max_q > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    if (cache->dt == KDA_E4M3 && cache->D == 64 && cache->page_size == 1) return KDA_ERR_UNSUPPORTED;   // boxes of 64 bytes
     if (num_seqs == 0 || total_tokens == 0) return KDA_OK;
     if (!q || !out || !aligned16(q) || !aligned16(out)) return KDA_ERR_INVALID_ARG;
     const uintptr_t words[] = {reinterpret_cast<uintptr_t>(alibi_slopes), reinterpret_cast<uintptr_t>(kv_start),
