@@ -240,11 +240,7 @@ struct Walk {
         }
         if (tid == THREADS - 1) work[groups] = before;
         __syncthreads();
-        const int64_t total = work[groups];
-        per = max((total + kWorkers - 1) / kWorkers, (int64_t)1);
-        begin = min((int64_t)blockIdx.x * per, total);
-        end = min(begin + per, total);
-        at = begin;
+        place(work[groups]);
         int gr = 0;   // the group that holds `at`: the last with work[gr] <= at
         for (int lo = 0, hi = groups - 1; lo <= hi;) {
             const int mid = (lo + hi) >> 1;
@@ -252,9 +248,53 @@ struct Walk {
         }
         n = gr * per_group;
         base = work[gr];
-        item = -1;
         __syncthreads();
     }
+    // With up to 32 sequences each warp that walks knows them all, a lane each: no barrier, no table, and
+    // no loads when the walk comes to the next one.  8 sequences of up to 300 keys took PENDING us with the
+    // table, PENDING us so.
+    static constexpr int kFew = 32;
+    Seq lanes;
+    __device__ __forceinline__ bool few() const { return P.num_seqs <= kFew; }
+    __device__ __forceinline__ void find_few(int lane) {
+        lanes = {};
+        if (lane < P.num_seqs) lanes = seq_info<TOK>(P, lane, ROWS);
+        const int64_t mine = units(lanes) * lanes.blocks * P.c.Hkv;
+        int64_t behind = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, behind, o);
+            if (lane >= o) behind += x;
+        }
+        place(__shfl_sync(0xffffffffu, behind, 31));
+        const unsigned m = __ballot_sync(0xffffffffu, behind - mine <= at && lane < P.num_seqs);
+        n = 31 - __clz(m);   // lane 0 holds place 0
+        base = __shfl_sync(0xffffffffu, behind - mine, n);
+    }
+    // This worker's stretch of `total` units.
+    __device__ __forceinline__ void place(int64_t total) {
+        per = max((total + kWorkers - 1) / kWorkers, (int64_t)1);
+        begin = min((int64_t)blockIdx.x * per, total);
+        end = min(begin + per, total);
+        at = begin;
+        item = -1;
+    }
+    // Sequence n, by all lanes.
+    __device__ __forceinline__ Seq sequence() const {
+        if (!few()) return seq_info<TOK>(P, n, ROWS);
+        Seq q;
+        q.t0 = __shfl_sync(0xffffffffu, lanes.t0, n);
+        q.nq = __shfl_sync(0xffffffffu, lanes.nq, n);
+        q.pos0 = __shfl_sync(0xffffffffu, lanes.pos0, n);
+        q.start = __shfl_sync(0xffffffffu, lanes.start, n);
+        q.lo = __shfl_sync(0xffffffffu, lanes.lo, n);
+        q.hi = __shfl_sync(0xffffffffu, lanes.hi, n);
+        q.tile0 = __shfl_sync(0xffffffffu, lanes.tile0, n);
+        q.tiles = __shfl_sync(0xffffffffu, lanes.tiles, n);
+        q.blocks = __shfl_sync(0xffffffffu, lanes.blocks, n);
+        return q;
+    }
+
     // Units of an item of a sequence.
     static __device__ __forceinline__ int64_t units(const Seq& q) { return q.tiles + kItemCost; }
     // The item that holds `at`; false if nothing of its tiles lies in the stretch.
@@ -264,7 +304,7 @@ struct Walk {
         while (at - base >= items * units(s)) {
             base += items * units(s);
             ++n;
-            s = seq_info<TOK>(P, n, ROWS);
+            s = sequence();
             items = (int64_t)s.blocks * P.c.Hkv;
         }
         const int x = quotient(at - base, units(s));
@@ -406,7 +446,8 @@ struct Fetch {
     // Finds the first tile; false if the stretch has none.
     __device__ __forceinline__ bool begin(W& w) {
         if (keys && lane == 0) P.split[blockIdx.x].last = -1;
-        w.s = seq_info<C::TOK>(P, w.n, ROWS);
+        if (w.few()) w.find_few(lane);
+        w.s = w.sequence();
         if (!w.seek()) return false;
         if (keys && lane == 0) w.tell_join(P.split + blockIdx.x);
         look(w);

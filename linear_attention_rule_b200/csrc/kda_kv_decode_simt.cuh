@@ -218,7 +218,7 @@ struct SimtKernel {
         if (tid == 0) { prefetch_map(&P.k_map); prefetch_map(&P.v_map); prefetch_map(&P.q_map); }
         kda_grid_wait();
         W w(P);
-        w.template find<C::THREADS>(reinterpret_cast<int64_t*>(sm));
+        if (!w.few()) w.template find<C::THREADS>(reinterpret_cast<int64_t*>(sm));
         kda_grid_launch_next();
         Fetch<C, R> f{P, lane, warp == C::CW, {}};
         if (warp >= C::CW) {

@@ -714,7 +714,7 @@ struct TcKernel {
         if (tid == 0) { prefetch_map(&P.k_map); prefetch_map(&P.v_map); prefetch_map(&P.q_map); }
         kda_grid_wait();
         W w(P);
-        w.template find<C::THREADS>(reinterpret_cast<int64_t*>(sm + C::RING));
+        if (!w.few()) w.template find<C::THREADS>(reinterpret_cast<int64_t*>(sm + C::RING));
         kda_grid_launch_next();
         Fetch<C, N> f{P, lane, warp == C::SW, {}};
         if (warp == 0) sm100::tmem_alloc(sb + C::TMEM, C::TCOLS);
