@@ -364,7 +364,7 @@ kda_status kda_prefill_noalloc(const void *q, const void *k, const void *v, cons
  *   - The new tokens are packed: sequence n has the tokens cu_seqlens[n] .. cu_seqlens[n+1]-1
  *     of the [total_tokens, ...] arrays, possibly none.  cu_seqlens (int32 [num_seqs + 1],
  *     device) starts at 0, does not fall and ends at or below total_tokens; tokens behind its
- *     last entry are padding, neither read nor written.  NULL means one token per sequence
+ *     last entry are padding: what they hold has no effect, and nothing is written for them.  NULL means one token per sequence
  *     (num_seqs == total_tokens).  A sequence whose entries break this is skipped and
  *     reported as KDA_ERR_BAD_SEQLENS.
  *   - q, k and v may be slices of one projection: the head and channel axes are dense, and
@@ -489,8 +489,13 @@ kda_status kda_kv_append(const void *k, const void *v, const void *q, int64_t k_
  *                 contents do not matter, clobbered, one for each call in flight
  * Visible positions outside the block table, or on a page outside the cache, are left out
  * of the sums and reported as KDA_ERR_BAD_PAGE.  Scores, their statistics and the sums are
- * fp32; with bf16 queries the softmax weights are rounded to the type that multiplies the
- * values (bf16, or fp16 over a KDA_E4M3 cache).
+ * fp32; with bf16 queries the softmax weights are rounded to bf16, or to fp16 over a
+ * KDA_E4M3 cache (and to 2^-25 of the row's largest), where a query's channels are held to
+ * 2^-22 of its largest.  A query with an infinity gets NaN there.  Keys outside what a token
+ * sees may be read where they share a page with ones that it sees.  The sums' order depends
+ * on the call's sizes and lengths alone: the same call gives the same bits.
+ * Not supported (KDA_ERR_UNSUPPORTED): pages of one row in a KDA_E4M3 cache of 64 channels;
+ * strides of 2^40 bytes and more.
  */
 kda_status kda_kv_decode(const void *q, int64_t q_stride, kda_dtype dt, const kda_kv_cache *cache,
                          const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,

@@ -23,7 +23,12 @@
 //   a weight, in fp16 (2^-11), is p1 + p2 / 16 + p3 / 256 exactly, down to 2^-25 of the row's largest.
 // The products are exact and summed in fp32: 2^-25 of the sum of magnitudes over 128 products.  The
 // other way, turning the cache's tiles into fp16 images, took eight warps 1,900 cycles an operand and
-// four times the shared-memory traffic: 151 us for 75,800 keys of 8 heads.
+// four times the shared-memory traffic: 151 us for 75,800 keys of 8 heads, now 80.
+//
+// A product with M = 128 takes 124 cycles whatever its type, its operands' order and N up to 48 (measured), 16 of
+// them a bf16 tile of 128 channels: 1,980 of the 2,780 cycles in which an SM's share of the memory brings it.  A
+// softmax warp's way through a tile takes about 1,900.  So bf16 is bound by memory (6.1 to 6.4 TB/s over long
+// sequences), e4m3 by that way, at 2,100 cycles a tile where the memory would need 1,390 (4.4 TB/s).
 #pragma once
 
 #include "kda_kv_decode.cuh"
