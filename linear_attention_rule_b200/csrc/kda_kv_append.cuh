@@ -11,8 +11,8 @@
 // A warp has one token, or every 2nd or 4th part of one where there are few tokens.  Its lanes hold the
 // same channels of several heads, so that a lane's sines and cosines stay in registers; the first
 // loads are on their way before the token's sequence, page and angles are known.  With a CTA per token,
-// a table of sines in shared memory and the loads behind it, 8,550 tokens of 16 + 2 x 4 heads took 48 us, now 28.5;
-// 25,000 of 32 + 2 x 8 heads took 164 us, now 139 (6.2 TB/s).
+// a table of sines in shared memory and the loads behind it, 9,221 tokens of 16 + 2 x 4 heads took 48 us, now 28.5;
+// 34,953 of 32 + 2 x 8 heads took 164 us, now 139 (6.2 TB/s).
 #pragma once
 
 #include "kda_kv_cache.cuh"
@@ -289,7 +289,7 @@ template <int D, typename T, typename TC>
 cudaError_t launch(Params& P, cudaStream_t stream) {
     // Few tokens are shared by several warps each, so that the heads of one do not queue behind each other (a
     // call by itself): 64 tokens take 14.3 us by one warp each, 10.2 by four, 600 tokens 16.4 and 12.3; 1,500
-    // tokens take 18.4 by one, 16.4 by two, 18.4 by four; prompts of 25,000 145 by one, 158 by four.
+    // tokens take 18.4 by one, 16.4 by two, 18.4 by four; prompts of 34,953 145 by one, 158 by four.
     P.parts = P.total >= 148 * 16 ? 1 : P.total >= 148 * 8 ? 2 : 4;
     const int64_t blocks = (P.total * P.parts + kWarps - 1) / kWarps;
     return kda_launch_chained(append_kernel<D, T, TC>, dim3((unsigned)blocks), 32 * kWarps, 0, stream, P);

@@ -1,5 +1,5 @@
 // Argument marshalling of the calls of a decode step, whose kernels take a few microseconds: through
-// ctypes the checks and conversions of 20 arguments took 9 to 12 us a call, here they take under one.
+// ctypes a call took 16 to 20 us of host time, here 3.6 (an append) to 7.2 (a pool's step), launch included.
 // The functions check torch tensors, take their pointers and call libkda's C entry points, whose
 // addresses init() is given; they return the status.  No computation, no fallback.
 #include <torch/csrc/autograd/python_variable.h>
