@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
 // values are read once.  4 rows as 32 took 17.4 us instead of 15.2 over 8 short sequences, one row of fp32 as
 // 8 took 33.8 us instead of 29.7; 64 rows in two blocks of 32 took 152 us instead of 119.
 inline int block_rows(bool f32, int rows) {
-    return f32 ? (rows <= 2 ? 2 : 8) : (rows <= 16 ? 16 : rows <= 32 ? 32 : 64);
+    return f32 ? (rows == 1 ? 1 : rows == 2 ? 2 : 8) : (rows <= 16 ? 16 : rows <= 32 ? 32 : 64);
 }
 inline size_t header_bytes() { return (sizeof(Split) * kWorkers + 255) & ~(size_t)255; }
 inline size_t workspace_bytes(int D, int rows) {

@@ -8,6 +8,8 @@
 // a warp per row and another barrier a tile took half as long again.
 #pragma once
 
+#include <type_traits>
+
 #include "kda_kv_decode.cuh"
 
 namespace kda {
@@ -78,7 +80,13 @@ struct SimtKernel {
         const int key = w * C::KPW + (C::PARTS == 4 ? (gr >> 1) | ((gr & 1) << 2) : gr);
         const int d = tid % D, kg = tid / D;
         float* pw = reinterpret_cast<float*>(sm + C::PW) + w * R * TOK;   // the warp's copy of the weights
-        float acc[R], m[R], l[R], slope[R];   // l: this lane's keys
+        // Rows go by groups of G without a branch between them, so that their chains overlap; those of a
+        // group behind the block's last row are zeros and go nowhere.  After the sums a lane
+        // has the score of row part % G of each group.
+        constexpr int G = R < 4 ? R : 4, GS = R / G;
+        const int mine = part & (G - 1);
+        float acc[R], m[R], l[R], slope[GS];   // l: this lane's keys
+        int tok[GS];
         bool bad = false;
         for (int t = 0;; ++t) {
             bad |= !wait_warp(sb + C::FULL + 8 * (t % C::STG), (t / C::STG) & 1);
@@ -98,7 +106,12 @@ struct SimtKernel {
                     acc[r] = 0.f;
                     m[r] = -INFINITY;
                     l[r] = 0.f;
-                    slope[r] = P.slopes && r < mt.rows ? P.slopes[mt.h * P.group + (mt.block * R + r) % P.group] * kLog2e : 0.f;
+                }
+#pragma unroll
+                for (int g = 0; g < GS; ++g) {
+                    const int r = g * G + mine;
+                    slope[g] = P.slopes && r < mt.rows ? P.slopes[mt.h * P.group + (mt.block * R + r) % P.group] * kLog2e : 0.f;
+                    tok[g] = mt.tok0 + (r < mt.left0 ? 0 : 1 + (r - mt.left0) / P.group);
                 }
             }
             {   // scores, in units of log 2; -infinity where the row does not see the key
@@ -107,51 +120,67 @@ struct SimtKernel {
                 for (int i = 0; i < 4; ++i) kk[i] = *reinterpret_cast<const float4*>(k + chunk(key, i * C::PARTS + part));
                 const int j = mt.j0 + key;
                 const bool ok = (okm[key >> 5] >> (key & 31)) & 1;
-                int tok = mt.tok0, left = mt.left0;
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    if (r >= mt.rows) break;
-                    float x[4];   // four short chains
+                for (int g = 0; g < GS; ++g) {
+                    if (g * G >= mt.rows) break;
+                    float y[G];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 a = *reinterpret_cast<const float4*>(q + r * D + (i * C::PARTS + part) * 4);
-                        x[i] = a.x * kk[i].x + a.y * kk[i].y + a.z * kk[i].z + a.w * kk[i].w;
+                    for (int r = 0; r < G; ++r) {
+                        float x[4];   // four short chains
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float4 a = *reinterpret_cast<const float4*>(q + (g * G + r) * D + (i * C::PARTS + part) * 4);
+                            x[i] = a.x * kk[i].x + a.y * kk[i].y + a.z * kk[i].z + a.w * kk[i].w;
+                        }
+                        y[r] = (x[0] + x[1]) + (x[2] + x[3]);
                     }
-                    float y = (x[0] + x[1]) + (x[2] + x[3]);
+                    // lanes that differ in a bit exchange the halves of their rows, then sum up what is left
+                    int o = 1;
 #pragma unroll
-                    for (int o = 1; o < C::PARTS; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-                    const int p = mt.pos0 + tok;
-                    if (part == r % C::PARTS) {
-                        y *= P.scale;
-                        if (P.softcap > 0.f) y = P.softcap * tanhf(y / P.softcap);
-                        y = y * kLog2e + slope[r] * (float)(j - p);
-                        if (!ok || (edge && (j > p || j < first_key(P, mt.start, p)))) y = -INFINITY;
-                        sc[r * TOK + key] = y;
+                    for (int n = G; n > 1; n >>= 1, o <<= 1) {
+                        const bool odd = part & o;
+#pragma unroll
+                        for (int r = 0; r < n / 2; ++r) {
+                            const float keep = odd ? y[2 * r + 1] : y[2 * r], give = odd ? y[2 * r] : y[2 * r + 1];
+                            y[r] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                        }
                     }
-                    if (--left == 0) { ++tok; left = P.group; }
+#pragma unroll
+                    for (; o < C::PARTS; o <<= 1) y[0] += __shfl_xor_sync(0xffffffffu, y[0], o);
+                    if (part < G) {
+                        const int pos = mt.pos0 + tok[g];
+                        float z = y[0] * P.scale;
+                        if (P.softcap > 0.f) z = P.softcap * tanhf(z / P.softcap);
+                        z = z * kLog2e + slope[g] * (float)(j - pos);
+                        if (!ok || (edge && (j > pos || j < first_key(P, mt.start, pos)))) z = -INFINITY;
+                        sc[(g * G + mine) * TOK + key] = z;
+                    }
                 }
             }
             if (bar_any(1, bad || aborted(), NT)) break;
             float f[R];
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                if (r >= mt.rows) break;
-                float x[TOK / 32], top = -INFINITY;
+            for (int g = 0; g < GS; ++g) {
+                if (g * G >= mt.rows) break;
 #pragma unroll
-                for (int i = 0; i < TOK / 32; ++i) {
-                    x[i] = sc[r * TOK + 32 * i + lane];
-                    top = fmaxf(top, x[i]);
-                }
-                top = fmaxf(m[r], warp_max(top));
-                f[r] = m[r] == -INFINITY ? 0.f : ex2(m[r] - top);
-                const float ms = top == -INFINITY ? 0.f : top;
-                m[r] = top;
-                l[r] *= f[r];
+                for (int r = g * G; r < g * G + G; ++r) {
+                    float x[TOK / 32], top = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < TOK / 32; ++i) {
-                    const float p = ex2(x[i] - ms);
-                    l[r] += p;
-                    pw[r * TOK + 32 * i + lane] = x[i] == -INFINITY ? -0.f : p;   // -0: takes nothing of the value
+                    for (int i = 0; i < TOK / 32; ++i) {
+                        x[i] = sc[r * TOK + 32 * i + lane];
+                        top = fmaxf(top, x[i]);
+                    }
+                    top = fmaxf(m[r], warp_max(top));
+                    f[r] = m[r] == -INFINITY ? 0.f : ex2(m[r] - top);
+                    const float ms = top == -INFINITY ? 0.f : top;
+                    m[r] = top;
+                    l[r] *= f[r];
+#pragma unroll
+                    for (int i = 0; i < TOK / 32; ++i) {
+                        const float p = ex2(x[i] - ms);
+                        l[r] += p;
+                        pw[r * TOK + 32 * i + lane] = x[i] == -INFINITY ? -0.f : p;   // -0: takes nothing of the value
+                    }
                 }
             }
             __syncwarp();
@@ -159,22 +188,30 @@ struct SimtKernel {
                 float vv[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) vv[i] = *reinterpret_cast<const float*>(v + chunk(kg * 16 + i, d >> 2) + (d & 3) * 4);
+                const auto values = [&](auto some) {   // some: of rows that may not see a key
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    if (r >= mt.rows) break;
-                    float a[4] = {acc[r] * f[r], 0.f, 0.f, 0.f};
+                    for (int g = 0; g < GS; ++g) {
+                        if (g * G >= mt.rows) break;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 p = *reinterpret_cast<const float4*>(pw + r * TOK + kg * 16 + 4 * i);
-                        const float pp[4] = {p.x, p.y, p.z, p.w};
+                        for (int r = g * G; r < g * G + G; ++r) {
+                            float a[4] = {acc[r] * f[r], 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            // a row that does not see the key takes nothing of its value, be it NaN
-                            if (!edge || __float_as_uint(pp[e]) != 0x80000000u) a[i] += pp[e] * vv[4 * i + e];
+                            for (int i = 0; i < 4; ++i) {
+                                const float4 p = *reinterpret_cast<const float4*>(pw + r * TOK + kg * 16 + 4 * i);
+                                const float pp[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    // a row that does not see the key takes nothing of its value, be it NaN
+                                    const float with = fmaf(pp[e], vv[4 * i + e], a[i]);
+                                    a[i] = decltype(some)::value && __float_as_uint(pp[e]) == 0x80000000u ? a[i] : with;
+                                }
+                            }
+                            acc[r] = (a[0] + a[1]) + (a[2] + a[3]);
                         }
                     }
-                    acc[r] = (a[0] + a[1]) + (a[2] + a[3]);
-                }
+                };
+                if (edge) values(std::true_type());
+                else values(std::false_type());
             }
             __syncwarp();
             if (lane == 0) sm100::mbar_arrive(sb + C::EMPTY + 8 * (t % C::STG));

@@ -795,7 +795,7 @@ template <int D, typename T, typename TC>
 cudaError_t launch(Params& P, cudaStream_t stream) {
     const int rows = block_rows(sizeof(T) == 4, P.group * P.max_q);
     if constexpr (sizeof(T) == 4)
-        return rows == 2 ? launch_simt<D, 2>(P, stream) : launch_simt<D, 8>(P, stream);
+        return rows == 1 ? launch_simt<D, 1>(P, stream) : rows == 2 ? launch_simt<D, 2>(P, stream) : launch_simt<D, 8>(P, stream);
     else
         return rows == 16 ? launch_tc<D, TC, 16>(P, stream) : rows == 32 ? launch_tc<D, TC, 32>(P, stream) : launch_tc<D, TC, 64>(P, stream);
 }
