@@ -520,7 +520,7 @@ def kda_kv_decode(q, k_cache, v_cache, block_table, seq_lens, out, cu_seqlens=No
     if workspace is None and isinstance(q, torch.Tensor) and isinstance(k_cache, torch.Tensor):
         # bad shapes get none, and the call below says what is wrong with them
         Hq, Hkv, D = (q.shape[1], k_cache.shape[1], q.shape[2]) if q.dim() == 3 and k_cache.dim() == 4 else (0, 0, 0)
-        N = q.shape[0] if cu_seqlens is None else max(cu_seqlens.numel() - 1, 0)
+        N = max(cu_seqlens.numel() - 1, 0) if isinstance(cu_seqlens, torch.Tensor) else 0 if q.dim() == 0 else q.shape[0]
         with torch.cuda.stream(stream):   # None: the current stream
             workspace = torch.empty(kda_kv_decode_workspace_size(N, Hq, Hkv, D, max_q), dtype=torch.uint8, device=q.device)
     st = native.kv_decode(q, k_cache, v_cache, block_table, seq_lens, out, cu_seqlens, max_q, scale, softcap, window,

@@ -67,6 +67,24 @@ def test_row_blocks_split_over_stretches(dtype, cdt, D, Hq, Hkv, new):
         assert torch.equal(out, o2) and torch.equal(lse, l2)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,new", [(2, 1), (2, 2), (6, 1), (8, 1), (10, 1), (8, 2), (6, 3)])
+def test_fp32_rows_in_groups(D, Hq, new):
+    """1 to 9 rows a kv head: one row, two, groups of four that are full or not; sequences without a visible
+    key, split ones, and bad values where a row does not see."""
+    seq, lens = [2500, 3 + new, 190, 64], [new, new, 1, new]
+    q, kc, vc, table, sl, _ = _attend_inputs(F32, F32, D, Hq, 2, 16, "heads", seq, lens)
+    slopes = 0.5 ** torch.arange(1, Hq + 1, device="cuda", dtype=torch.float32)
+    _matches(q, kc, vc, table, sl, lens, None, None, slopes=slopes, start=[0, 2, 190, 63])
+    _matches(q, kc, vc, table, sl, lens, None, None, cap=4.0, window=70, slopes=slopes, start=[2400, 0, 7, 64])
+    clean, _ = _attend(q, kc, vc, table, sl, lens, None, None, kv_start=_ints([2450, 0, 0, 60]))
+    for c in (kc, vc):   # before the first visible keys, in their pages
+        c[table[0, 2449 // 16].long(), :, : 2450 % 16] = math.nan
+        c[table[3, 59 // 16].long(), :, : 60 % 16] = -math.inf
+    out, _ = _attend(q, kc, vc, table, sl, lens, None, None, kv_start=_ints([2450, 0, 0, 60]))
+    assert torch.equal(out, clean)
+
+
 @pytest.mark.parametrize("dtype,cdt", [(BF16, BF16), (BF16, E4M3), (F32, F32)])
 def test_many_short_sequences(dtype, cdt):
     """More sequences than the table of work has entries, a third of them without new tokens."""

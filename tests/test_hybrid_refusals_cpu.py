@@ -210,3 +210,10 @@ def test_decode_binding_checks(bad, exc, match):
     a.update(bad)
     with pytest.raises(exc, match=match):
         kda.kda_kv_decode(**a)
+
+
+@pytest.mark.parametrize("cu", [[0, 1, 2, 3, 4], 4])
+def test_decode_without_a_workspace_names_a_bad_argument(cu):
+    with pytest.raises(ValueError, match="cu_seqlens"):
+        kda.kda_kv_decode(q=torch.zeros(4, 4, 64), k_cache=torch.zeros(6, 2, 16, 64), v_cache=torch.zeros(6, 2, 16, 64),
+                          block_table=_ints(4, 3), seq_lens=_ints(4), out=torch.zeros(4, 4, 64), cu_seqlens=cu)
