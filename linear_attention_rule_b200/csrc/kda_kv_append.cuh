@@ -209,7 +209,8 @@ struct Token {
         const T* src = static_cast<const T*>(P.q) + t * P.q_stride + c0;
         T* dst = static_cast<T*>(P.q_out) + t * P.Hq * D + c0;
         for (int h = first; h < P.Hq; h += 2 * step) {
-            if (h != first) fetch(src, h, P.Hq, a, b);
+            Raw na[2], nb[2];   // the next heads, on their way meanwhile
+            fetch(src, h + 2 * step, P.Hq, na, nb);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 float x[8], y[8];
@@ -219,6 +220,8 @@ struct Token {
                 Vec8<T>::store(at, x);
                 if (two) Vec8<T>::store(at + half, y);
             }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) { a[i] = na[i]; b[i] = nb[i]; }
         }
     }
     __device__ __forceinline__ void keys(int64_t row) const {
