@@ -11,8 +11,9 @@
 // A warp has one token, or every 2nd or 4th part of one where there are few tokens.  Its lanes hold the
 // same channels of several heads, so that a lane's sines and cosines stay in registers; the first
 // loads are on their way before the token's sequence, page and angles are known.  With a CTA per token,
-// a table of sines in shared memory and the loads behind it, 9,221 tokens of 16 + 2 x 4 heads took 48 us, now 28.5;
-// 34,953 of 32 + 2 x 8 heads took 164 us, now 139 (6.2 TB/s).
+// a table of sines in shared memory and the loads behind it, 9,221 tokens of 16 + 2 x 4 heads took 48 us, now 25.9;
+// 34,953 of 32 + 2 x 8 heads took 164 us, now 139 (6.2 TB/s).  Keys and values brought to L2 ahead by a
+// prefetch made the latter 155.
 #pragma once
 
 #include "kda_kv_cache.cuh"
@@ -205,23 +206,46 @@ struct Token {
         }
         Vec8<TC>::store(dst, x);
     }
+    // The next heads are on their way while two are turned: two more with AHEAD, else each head's as soon as
+    // its registers are free.
+    template <bool AHEAD>
     __device__ __forceinline__ void queries(Raw (&a)[2], Raw (&b)[2]) const {
         const T* src = static_cast<const T*>(P.q) + t * P.q_stride + c0;
         T* dst = static_cast<T*>(P.q_out) + t * P.Hq * D + c0;
-        for (int h = first; h < P.Hq; h += 2 * step) {
-            Raw na[2], nb[2];   // the next heads, on their way meanwhile
-            fetch(src, h + 2 * step, P.Hq, na, nb);
+        if constexpr (AHEAD) {
+            for (int h = first; h < P.Hq; h += 2 * step) {
+                Raw na[2], nb[2];
+                fetch(src, h + 2 * step, P.Hq, na, nb);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float x[8], y[8];
-                if (!mine || h + i * step >= P.Hq) continue;
-                turn(a[i], b[i], x, y);
-                T* at = dst + (int64_t)(h + i * step) * D;
-                Vec8<T>::store(at, x);
-                if (two) Vec8<T>::store(at + half, y);
+                for (int i = 0; i < 2; ++i) {
+                    float x[8], y[8];
+                    if (!mine || h + i * step >= P.Hq) continue;
+                    turn(a[i], b[i], x, y);
+                    T* at = dst + (int64_t)(h + i * step) * D;
+                    Vec8<T>::store(at, x);
+                    if (two) Vec8<T>::store(at + half, y);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) { a[i] = na[i]; b[i] = nb[i]; }
             }
+        } else {
+            for (int h = first; h < P.Hq; h += 2 * step) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) { a[i] = na[i]; b[i] = nb[i]; }
+                for (int i = 0; i < 2; ++i) {
+                    float x[8], y[8];
+                    const int now = h + i * step, next = now + 2 * step;
+                    if (!mine || now >= P.Hq) continue;
+                    turn(a[i], b[i], x, y);
+                    if (next < P.Hq) {
+                        const T* from = src + (int64_t)next * D;
+                        a[i] = Vec8<T>::fetch(from);
+                        if (two) b[i] = Vec8<T>::fetch(from + half);
+                    }
+                    T* at = dst + (int64_t)now * D;
+                    Vec8<T>::store(at, x);
+                    if (two) Vec8<T>::store(at + half, y);
+                }
+            }
         }
     }
     __device__ __forceinline__ void keys(int64_t row) const {
@@ -263,7 +287,7 @@ struct Token {
     }
 };
 
-template <int D, typename T, typename TC>
+template <int D, typename T, typename TC, bool AHEAD>
 __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 8 : 6) append_kernel(const __grid_constant__ Params P) {
     typedef Token<D, T, TC> Tok;
     const int lane = threadIdx.x & 31;
@@ -282,7 +306,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 8 : 6) append_ke
     const int64_t row = kv::row_offset(P.c, n, pos, 0);
     if (row < 0 && lane == 0) kda_set_status(KDA_ERR_BAD_PAGE);
     if (P.rot) k.angles(pos);
-    if (P.q) k.queries(a, b);
+    if (P.q) k.template queries<AHEAD>(a, b);
     if (row < 0) return;
     k.keys(row);
     k.values(row);
@@ -295,7 +319,14 @@ cudaError_t launch(Params& P, cudaStream_t stream) {
     // tokens take 18.4 by one, 16.4 by two, 18.4 by four; prompts of 34,953 145 by one, 158 by four.
     P.parts = P.total >= 148 * 16 ? 1 : P.total >= 148 * 8 ? 2 : 4;
     const int64_t blocks = (P.total * P.parts + kWarps - 1) / kWarps;
-    return kda_launch_chained(append_kernel<D, T, TC>, dim3((unsigned)blocks), 32 * kWarps, 0, stream, P);
+    // Two heads further ahead where a bf16 token's heads are all one warp's: 34,953 tokens of 32 + 2 x 8 heads with
+    // neighbours paired take 147 us instead of 174, over e4m3 133 instead of 140.  It spills a few registers, which
+    // costs where the loop is short (1,500 tokens 7.6 us instead of 7.3) or a head takes twice the registers (fp32,
+    // 4 prompts: 192 us instead of 176).
+    if constexpr (sizeof(T) == 2)
+        if (P.parts == 1)
+            return kda_launch_chained(append_kernel<D, T, TC, true>, dim3((unsigned)blocks), 32 * kWarps, 0, stream, P);
+    return kda_launch_chained(append_kernel<D, T, TC, false>, dim3((unsigned)blocks), 32 * kWarps, 0, stream, P);
 }
 
 }  // namespace append
