@@ -22,24 +22,6 @@ __device__ __forceinline__ void kda_grid_wait() { asm volatile("griddepcontrol.w
 // Lets the next kernel of the stream be scheduled (its blocks wait at kda_grid_wait).
 __device__ __forceinline__ void kda_grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// Launches a kernel that begins with kda_grid_wait, so that its blocks are scheduled while the kernel
-// ahead of it in the stream ends.
-template <typename... Args>
-inline cudaError_t kda_launch_chained(void (*kernel)(Args...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
-                                      const Args&... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 // Input prologue (the layer's elementwise steps in front of KDA, fused into the kernels):
 // bit flags as in include/libkda.h (KDA_IN_*).
 constexpr uint32_t kInNormQK = 1u, kInGLogits = 2u, kInBetaLogits = 4u, kInGScalar = 8u,

@@ -13,7 +13,7 @@
 // 128 bytes instead of 64 and a sum over two warps 3 us.
 #pragma once
 
-#include "kda_common.cuh"
+#include "kda_launch.cuh"
 
 namespace kda {
 namespace pool {

@@ -3,7 +3,7 @@
 
 #include <cuda_fp8.h>
 
-#include "kda_common.cuh"
+#include "kda_launch.cuh"
 
 template <> __device__ __forceinline__ float to_f32<__nv_fp8_e4m3>(__nv_fp8_e4m3 x) { return static_cast<float>(x); }
 
