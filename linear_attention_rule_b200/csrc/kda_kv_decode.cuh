@@ -249,6 +249,8 @@ struct Walk {
         }
         n = gr * per_group;
         base = work[gr];
+        // TMA writes there next, through another proxy than these loads and stores, which a barrier alone does not order
+        sm100::fence_proxy_async_smem();
         __syncthreads();
     }
     // With up to 32 sequences each warp that walks knows them all, a lane each: no barrier, no table, and
