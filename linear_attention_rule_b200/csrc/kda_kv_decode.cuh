@@ -181,6 +181,10 @@ struct Meta {
     int32_t pad;
 };
 static_assert(sizeof(Meta) == 64, "laid out in shared memory");
+// Zeros, by one warp before the others look: a tile whose wait runs out is read as something valid.
+__device__ __forceinline__ void clear_meta(Meta* m, int count, int lane) {
+    for (int i = lane; i < count * (int)(sizeof(Meta) / 16); i += 32) reinterpret_cast<uint4*>(m)[i] = make_uint4(0u, 0u, 0u, 0u);
+}
 enum : int32_t { kFirst = 1, kLast = 2, kEdge = 4, kEnd = 8 };   // first, last tile of the item here; not all keys seen by all; last tile of all
 
 // The stretch of this worker, and the walk along its tiles.  An item takes a unit of the line for each of

@@ -425,29 +425,31 @@ struct TcKernel {
         float2* info = reinterpret_cast<float2*>(sm + C::RINFO) + row0;
         float* wred = reinterpret_cast<float*>(sm + C::WRED) + row0;
         float* frow = reinterpret_cast<float*>(sm + C::FROW) + row0;
-        const float cap2 = P.softcap * kLog2e;
+        const float cap2 = P.softcap * kLog2e, unit = P.scale * (P.softcap > 0.f ? 1.f / P.softcap : kLog2e);
         float l[RW];
         uint32_t pos = 0, neg = 0, events = 0;
         bool bad = false;
         for (int t = 0;; ++t) {
             bad |= !wait_warp(sb + C::MFULL + 8 * (t % C::MD), (t / C::MD) & 1);
+            // After a wait that ran out this is another tile's or zeros: addresses formed from it hold, and no
+            // barrier stands before the vote below, where the group of warps stops together.
             const Meta mt = *meta(t);
             const bool first = mt.flags & kFirst, edge = mt.flags & kEdge;
             const int rows = min(mt.rows - row0, RW);   // of these warps; maybe none
             if (first) {
                 if constexpr (F8) bad |= !wait_warp(sb + C::QFULL + 8 * (mt.item % C::QS), (mt.item / C::QS) & 1);
-                if (tid < RW) {
-                    mrow[tid] = make_float2(-INFINITY, 0.f);
-                    float f = P.scale * (P.softcap > 0.f ? 1.f / P.softcap : kLog2e), slope = 0.f;
-                    if (F8) f *= (P.c.k_scale ? P.c.k_scale[mt.h] : 1.f) * reinterpret_cast<const float*>(sm + C::QF)[(mt.item % C::QS) * N + row0 + tid];
-                    if (P.slopes && tid < rows) slope = P.slopes[mt.h * P.group + (mt.block * N + row0 + tid) % P.group] * kLog2e;
-                    info[tid] = make_float2(f, slope);   // scale of the raw products, bias per key
+                if (lane < RW) {   // every warp writes the same, so that no barrier stands before the vote
+                    mrow[lane] = make_float2(-INFINITY, 0.f);
+                    float f = unit, slope = 0.f;
+                    if (F8) f *= (P.c.k_scale ? P.c.k_scale[mt.h] : 1.f) * reinterpret_cast<const float*>(sm + C::QF)[(mt.item % C::QS) * N + row0 + lane];
+                    if (P.slopes && lane < rows) slope = P.slopes[mt.h * P.group + (mt.block * N + row0 + lane) % P.group] * kLog2e;
+                    info[lane] = make_float2(f, slope);   // scale of the raw products, bias per key
                 }
+                __syncwarp();
 #pragma unroll
                 for (int r = 0; r < RW; ++r) l[r] = 0.f;
                 pos = neg = 0;
             }
-            if (first) bar_all(bar, 128);
             bad |= !wait_warp(sb + C::SFULL + 8 * (t & 1), (t >> 1) & 1);
             tc_fence_after();
             const bool ok = (reinterpret_cast<const uint32_t*>(sm + C::OKM + (t % C::MD) * 16)[wq] >> lane) & 1;
@@ -723,6 +725,7 @@ struct TcKernel {
         kda_grid_launch_next();
         Fetch<C, N> f{P, lane, warp == C::SW, {}};
         if (warp == 0) sm100::tmem_alloc(sb + C::TMEM, C::TCOLS);
+        if (warp == 1) clear_meta(reinterpret_cast<Meta*>(sm + C::META), C::MD, lane);
         if (warp == C::SW || warp == C::SW + 1) {
             if (f.keys && lane == 0) {
                 for (int i = 0; i < C::STG; ++i) {

@@ -34,3 +34,22 @@ def test_first_tile_lands_where_the_table_of_work_lay(dtype, cdt):
         for _ in range(30):
             again, l2 = _attend(q, kc, vc, table, sl, ks, vs)
             assert torch.equal(out, again) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("cdt", [BF16, E4M3])
+@pytest.mark.parametrize("Hq,new", [(8, 1), (8, 4), (16, 4)])
+def test_items_of_one_tile_follow_one_another(cdt, Hq, new):
+    """Each warp sets an item's maxima and scales for itself.  Here each tile begins an item, and
+    queries alternate between large and small, so that a maximum or scale of the item before would show."""
+    N = 300
+    seq, lens = [new + n % 100 for n in range(N)], [new] * N
+    q, kc, vc, table, sl, (ks, vs) = _attend_inputs(BF16, cdt, 64, Hq, 1, 16, "heads", seq, lens)
+    q = (q.contiguous().unflatten(0, (N, new)) * torch.tensor([4.0, 2.0 ** -6], device="cuda").repeat(N // 2)[:, None, None, None]).flatten(0, 1).to(BF16)
+    cu = _cu(lens)
+    out, lse = _attend(q, kc, vc, table, sl, ks, vs, cu_seqlens=cu, max_q=new)
+    o, l, ob, lb = ref.attend(q, kc, vc, table, sl, lens, 64 ** -0.5, k_scale=ks, v_scale=vs)
+    _within(out, o, ob)
+    _within(lse, l, lb)
+    for _ in range(30):
+        again, l2 = _attend(q, kc, vc, table, sl, ks, vs, cu_seqlens=cu, max_q=new)
+        assert torch.equal(out, again) and torch.equal(lse, l2)
