@@ -15,6 +15,12 @@
 // of the next tile runs during the softmax of this one and the next item starts during the epilogue
 // of the last.  Tiles land in the operand images directly: TMA's swizzle is the images'.
 //
+// bf16: a weight rounded to 8 bits would be the largest error by far (0.0023 of an output's size where the rounding of the
+// output alone is 0.0017).  So it goes into the product in two bf16 parts side by side in N, 2^-16 of it, whose
+// columns are summed up at an item's end.  With the scores' arithmetic two rows at a time it takes the time that one part
+// took: 186 us for 64 sequences of 512 to 16,384 keys, 171 for 32 of 8,192 with 16 rows a kv head, 183 with 32 (one part 181),
+// 264 with 64, 107 with one row of 64 channels (106).
+//
 // e4m3: tcgen05 multiplies 8-bit with 8-bit operands only, and queries or weights rounded to 8 bits
 // would lose what the scores need.  So they are split into e4m3 parts that sum up to them, side by
 // side in N, which costs nothing while the long operand bounds the product:
@@ -45,7 +51,7 @@ struct Tc {
     static constexpr int RW = N == 64 ? 16 : 8, SW = 4 * N / RW;              // rows of four softmax warps, softmax warps
     static constexpr int LW = F8 ? 4 : 0;                                     // splitting warps
     static constexpr int THREADS = 32 * (SW + 3 + LW);
-    static constexpr int QP = F8 ? 2 : 1, PP = F8 ? 3 : 1;                    // parts of queries and weights
+    static constexpr int QP = F8 ? 2 : 1, PP = F8 ? 3 : 2;                    // parts of queries and weights
     // The running maximum follows the scores only when they exceed it by SLACK (in units of log 2):
     // until then acc is not rescaled.  Weights are 2^(s - m + BASE): up to 2^8, which fp32 sums and bf16
     // weights hold as well as 1; with e4m3 parts from 2^7 (the smallest parts then lie far below the
@@ -66,14 +72,17 @@ struct Tc {
     static constexpr int COLS = (2 * QP + OB * PP) * N;
     static constexpr int TCOLS = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
     // A stage is free when its tile is done; queries need one slot per stage, meta is read a little longer.
+    // Where that leaves two stages and two slots would leave three (32 bf16 rows of 128 channels: 187 us instead of 232),
+    // queries get two, and wait for the item before the last to be done.
     static constexpr int metas(int stg) { return stg + 2; }
     static constexpr int misc(int stg) {
         return metas(stg) * 64 + metas(stg) * 16 + stg * N * 4 + N * 8 + N * 8 + 4 * N * 4 + N * 4 + 8 * (4 * stg + metas(stg) + 13) + 16 + 4 * SW + stg * 4;
     }
-    static constexpr int total(int stg) { return stg * (STAGE + QB) + PB + misc(stg); }
-    static constexpr int most(int stg) { return stg > 2 && total(stg) > kMaxSmem ? most(stg - 1) : stg; }
-    static constexpr int STG = most(6), QS = STG, MD = metas(STG);
-    static constexpr int BYTES = total(STG);
+    static constexpr int total(int stg, int qs) { return stg * STAGE + qs * QB + PB + misc(stg); }
+    static constexpr int most(int stg) { return stg > 2 && total(stg, stg) > kMaxSmem ? most(stg - 1) : stg; }
+    static constexpr bool FEWQ = most(6) == 2 && total(3, 2) <= kMaxSmem;
+    static constexpr int STG = FEWQ ? 3 : most(6), QS = FEWQ ? 2 : STG, MD = metas(STG);
+    static constexpr int BYTES = total(STG, QS);
     static_assert(BYTES <= kMaxSmem, "shared memory of a CTA");
     static_assert((kGroups + 1) * 8 + 32 * 8 <= STG * STAGE, "the table of work lies where the ring comes");
     // offsets
@@ -138,6 +147,39 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
                  ::"r"(taddr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
                  : "memory");
 }
+// Two fp32 operations in one.
+__device__ __forceinline__ uint64_t bits2(float2 x) { return (uint64_t)__float_as_uint(x.y) << 32 | __float_as_uint(x.x); }
+__device__ __forceinline__ float2 of_bits2(uint64_t x) { return make_float2(__uint_as_float((uint32_t)x), __uint_as_float((uint32_t)(x >> 32))); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return of_bits2(r);
+}
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
+    uint64_t r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return of_bits2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return of_bits2(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+    return of_bits2(r);
+}
+__device__ __forceinline__ void load8(const float* from, float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+        const float4 u = *reinterpret_cast<const float4*>(from + i);
+        x[i] = u.x; x[i + 1] = u.y; x[i + 2] = u.z; x[i + 3] = u.w;
+    }
+}
+// A weight over a bf16 cache is its upper half and the rest, rounded to bf16.  The rest is taken 2^-19 of the weight
+// larger, so that it is positive where the weight is (an infinite value times a rest of 0 would be NaN).
+constexpr float kAbove1 = 1.f + 1.f / (1 << 19);
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) { return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3); }
 __device__ __forceinline__ uint32_t e4m3x2(__half2 x) { return __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3); }
 __device__ __forceinline__ __half2 half2_of(uint32_t e4m3x2) { return __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)e4m3x2, __NV_E4M3)); }
@@ -172,7 +214,9 @@ struct TcKernel {
         const bool ok = f.run(
             w,
             [&](int t) {
-                return !aborted() && (t < C::STG || wait_warp(sb + C::EMPTY + 8 * (t % C::STG), (t / C::STG - 1) & 1));
+                if (aborted() || (t >= C::STG && !wait_warp(sb + C::EMPTY + 8 * (t % C::STG), (t / C::STG - 1) & 1))) return false;
+                // queries into the slot of the item before the last: its tiles, up to t - 2 at most, are done
+                return !C::FEWQ || f.keys || w.i > 0 || w.item < C::QS || wait_warp(sb + C::EMPTY + 8 * ((t - 2) % C::STG), ((t - 2) / C::STG) & 1);
             },
             [&](int t) {
                 put(f, w, t);
@@ -404,15 +448,18 @@ struct TcKernel {
     // 8 rows of O^T, the parts summed up
     static __device__ __forceinline__ void load_out(uint32_t t, float (&o)[8]) {
         tmem_ld8(t, o);
+        float b[8];
+        tmem_ld8(t + N, b);
         if constexpr (F8) {
-            float b[8], c[8];
-            tmem_ld8(t + N, b);
+            float c[8];
             tmem_ld8(t + 2 * N, c);
             sm100::tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 8; ++i) o[i] += (b[i] + c[i] * (1.f / 16)) * (1.f / 16);
         } else {
             sm100::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] += b[i];
         }
     }
 
@@ -421,11 +468,13 @@ struct TcKernel {
         constexpr int RW = C::RW;
         const int wq = w & 3, row0 = (w >> 2) * RW, tid = 32 * wq + lane, key = tid;
         const uint32_t bar = 1 + (w >> 2), tl = tmem + ((uint32_t)(32 * wq) << 16);
-        float2* mrow = reinterpret_cast<float2*>(sm + C::MROW) + row0;   // (maximum + slack, maximum or 0)
-        float2* info = reinterpret_cast<float2*>(sm + C::RINFO) + row0;
+        float* limit = reinterpret_cast<float*>(sm + C::MROW) + row0;   // maximum + slack
+        float* base = limit + N;                                        // what a score's exponent counts from: maximum - BASE, or 0
+        float* unit = reinterpret_cast<float*>(sm + C::RINFO) + row0;   // scale of the raw products
+        float* slope = unit + N;                                        // bias per key
         float* wred = reinterpret_cast<float*>(sm + C::WRED) + row0;
         float* frow = reinterpret_cast<float*>(sm + C::FROW) + row0;
-        const float cap2 = P.softcap * kLog2e, unit = P.scale * (P.softcap > 0.f ? 1.f / P.softcap : kLog2e);
+        const float cap2 = P.softcap * kLog2e, scale = P.scale * (P.softcap > 0.f ? 1.f / P.softcap : kLog2e);
         float l[RW];
         uint32_t pos = 0, neg = 0, events = 0;
         bool bad = false;
@@ -439,11 +488,12 @@ struct TcKernel {
             if (first) {
                 if constexpr (F8) bad |= !wait_warp(sb + C::QFULL + 8 * (mt.item % C::QS), (mt.item / C::QS) & 1);
                 if (lane < RW) {   // every warp writes the same, so that no barrier stands before the vote
-                    mrow[lane] = make_float2(-INFINITY, 0.f);
-                    float f = unit, slope = 0.f;
+                    limit[lane] = -INFINITY;
+                    base[lane] = 0.f;
+                    float f = scale;
                     if (F8) f *= (P.c.k_scale ? P.c.k_scale[mt.h] : 1.f) * reinterpret_cast<const float*>(sm + C::QF)[(mt.item % C::QS) * N + row0 + lane];
-                    if (P.slopes && lane < rows) slope = P.slopes[mt.h * P.group + (mt.block * N + row0 + lane) % P.group] * kLog2e;
-                    info[lane] = make_float2(f, slope);   // scale of the raw products, bias per key
+                    unit[lane] = f;
+                    slope[lane] = P.slopes && lane < rows ? P.slopes[mt.h * P.group + (mt.block * N + row0 + lane) % P.group] * kLog2e : 0.f;
                 }
                 __syncwarp();
 #pragma unroll
@@ -478,45 +528,43 @@ struct TcKernel {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) s[c + i] += s2[i] * (1.f / 16);
                 }
-                float2 in[8];
-                float top[8];
-#pragma unroll
-                for (int i = 0; i < 8; i += 2) {   // two rows a load, the same for all lanes
-                    const float4 u = *reinterpret_cast<const float4*>(info + c + i);
-                    const float4 m = *reinterpret_cast<const float4*>(mrow + c + i);
-                    in[i] = make_float2(u.x, u.y);
-                    in[i + 1] = make_float2(u.z, u.w);
-                    top[i] = m.x;
-                    top[i + 1] = m.z;
-                }
+                float f[8], top[8];
+                load8(unit + c, f);   // the same for all lanes
+                load8(limit + c, top);
                 if (P.softcap > 0.f) {
                     // tanh y by its Taylor series up to y^9 where |y| <= 1/4 (the next term is below 2^-26 of it: most
                     // scores lie far below their cap, and no ex2 or rcp is spent on them), 1 - 2 / (1 + e^{2 y}) beyond
                     float big = 0.f;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float y = s[c + i] * in[i].x, z = y * y;
+                        const float y = s[c + i] * f[i], z = y * y;
                         const float tail = z * (-1.f / 3 + z * (2.f / 15 + z * (-17.f / 315 + z * (62.f / 2835))));
                         big = fmaxf(big, fabsf(y));
                         s[c + i] = fabsf(y) > 0.25f ? y : cap2 * (y + y * tail);
-                        in[i].x = y;
+                        f[i] = y;
                     }
                     if (__any_sync(0xffffffffu, big > 0.25f)) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const float y = in[i].x;
+                            const float y = f[i];
                             if (fabsf(y) > 0.25f) s[c + i] = cap2 - 2.f * cap2 * rcp(1.f + ex2(y * (2.f * kLog2e)));
                         }
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) s[c + i] *= in[i].x;
+                    for (int i = 0; i < 8; i += 2) {
+                        const float2 x = mul2(make_float2(s[c + i], s[c + i + 1]), make_float2(f[i], f[i + 1]));
+                        s[c + i] = x.x;
+                        s[c + i + 1] = x.y;
+                    }
                 }
                 if (P.slopes || mask) {
+                    float a[8];
+                    load8(slope + c, a);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int p = mt.pos0 + tok;
-                        s[c + i] += in[i].y * (float)(j - p);   // no bias: a slope of 0
+                        s[c + i] += a[i] * (float)(j - p);   // no bias: a slope of 0
                         s[c + i] = ok & sees(mt, j, p) ? s[c + i] : -INFINITY;
                         const bool over = --left == 0;
                         tok += over;
@@ -546,11 +594,12 @@ struct TcKernel {
                 bar_all(bar, 128);
                 if (tid < RW) {
                     const float top = fmaxf(fmaxf(wred[tid], wred[N + tid]), fmaxf(wred[2 * N + tid], wred[3 * N + tid]));
-                    const float2 old = mrow[tid];
+                    const float old = limit[tid];
                     float f = 1.f;
-                    if (top > old.x) {
-                        f = old.x == -INFINITY ? 0.f : ex2(old.y + C::BASE - top);
-                        mrow[tid] = make_float2(top + C::SLACK, top - C::BASE);
+                    if (top > old) {
+                        f = old == -INFINITY ? 0.f : ex2(base[tid] + C::BASE - top);
+                        limit[tid] = top + C::SLACK;
+                        base[tid] = top - C::BASE;
                     }
                     frow[tid] = f;
                 }
@@ -577,13 +626,16 @@ struct TcKernel {
 #pragma unroll
             for (int c = 0; c < RW; c += 8) {
                 if (c >= rows) break;
-                uint32_t pk[4], part[3][2] = {};
+                uint32_t pk[2][4], part[3][2] = {};
+                float m[8];
+                load8(base + c, m);
 #pragma unroll
                 for (int i = 0; i < 8; i += 2) {
-                    const float4 m = *reinterpret_cast<const float4*>(mrow + c + i);
-                    const float a = ex2(s[c + i] - m.y), b = ex2(s[c + i + 1] - m.w);
-                    l[c + i] += a;
-                    l[c + i + 1] += b;
+                    const float2 x = sub2(make_float2(s[c + i], s[c + i + 1]), make_float2(m[i], m[i + 1]));
+                    const float a = ex2(x.x), b = ex2(x.y);
+                    const float2 sum = add2(make_float2(l[c + i], l[c + i + 1]), make_float2(a, b));
+                    l[c + i] = sum.x;
+                    l[c + i + 1] = sum.y;
                     if constexpr (F8) {   // remainders are exact: fp16 has 11 bits, each part takes 4 and the sign
                         const __half2 k16 = __float2half2_rn(16.f);
                         __half2 r = __floats2half2_rn(a, b);
@@ -594,7 +646,11 @@ struct TcKernel {
                             if (y < 2) r = __hmul2(__hsub2(r, half2_of(e)), k16);
                         }
                     } else {
-                        pk[i / 2] = pack_bf16x2(a, b);
+                        const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+                        pk[0][i / 2] = __byte_perm(ua, ub, 0x7632);
+                        const float2 rest = fma2(make_float2(a, b), make_float2(kAbove1, kAbove1),
+                                                 make_float2(-__uint_as_float(ua & 0xffff0000u), -__uint_as_float(ub & 0xffff0000u)));
+                        pk[1][i / 2] = pack_bf16x2(rest.x, rest.y);
                     }
                 }
                 uint8_t* at = sm + C::PM + (row0 + c) / C::PG * (TOK * 16) + key * 16;
@@ -603,7 +659,9 @@ struct TcKernel {
                     for (int y = 0; y < 3; ++y)
                         *reinterpret_cast<uint2*>(at + y * (N / 16) * (TOK * 16) + (row0 + c) % 16) = make_uint2(part[y][0], part[y][1]);
                 } else {
-                    *reinterpret_cast<uint4*>(at) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        *reinterpret_cast<uint4*>(at + y * (N / 8) * (TOK * 16)) = make_uint4(pk[y][0], pk[y][1], pk[y][2], pk[y][3]);
                 }
             }
             if (!ok && row0 == 0) {   // a value row that was not fetched, or that no token sees
@@ -649,8 +707,7 @@ struct TcKernel {
             float sum = 0.f, top = 0.f;
             if (tid < rows) {
                 sum = wred[tid] + wred[N + tid] + wred[2 * N + tid] + wred[3 * N + tid];
-                const float2 m = mrow[tid];
-                top = m.x == -INFINITY ? -INFINITY : m.y;
+                top = limit[tid] == -INFINITY ? -INFINITY : base[tid];
                 const float vs = F8 && P.c.v_scale ? P.c.v_scale[mt.h] : 1.f;
                 frow[tid] = mt.part >= 0 ? 1.f : sum == 0.f ? 0.f : vs / sum;
             }

@@ -53,3 +53,44 @@ def test_items_of_one_tile_follow_one_another(cdt, Hq, new):
     for _ in range(30):
         again, l2 = _attend(q, kc, vc, table, sl, ks, vs, cu_seqlens=cu, max_q=new)
         assert torch.equal(out, again) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("Hq,new", [(4, 1), (8, 4), (16, 4)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_bf16_attention_is_the_formula_rounded_once(D, Hq, new):
+    """Over a bf16 cache weights go into the product with the values in two parts, cut off to 8 bits and the
+    rest rounded: 2^-16 of a weight (half a step of a rest below 2^-7 of it); the rest is taken 2^-19 of
+    the weight larger.  Beside the bounds of scores and sums, one rounding of the output is left
+    (2^-8 of it): not the 2^-8 of sum p |v| that weights of 8 bits would bring."""
+    seq, lens = [700, 64 + new, 2100, new], [new] * 4
+    q, kc, vc, table, sl, _ = _attend_inputs(BF16, BF16, D, Hq, 1, 32, "heads", seq, lens)
+    out, lse = _attend(q, kc, vc, table, sl, cu_seqlens=_cu(lens), max_q=new)
+    o, l, ob, lb = ref.attend(q, kc, vc, table, sl, lens, D ** -0.5)
+    # sum p |v|: the attention of the values' sizes
+    size = ref.attend(q, kc, vc.abs(), table, sl, lens, D ** -0.5)[0]
+    # ob = (1 + h) (arithmetic + 2^-8 size) + h |o|, h = 2^-8, with the weights' rounding taken as 2^-8
+    h = 2.0 ** -8
+    arithmetic = (ob - h * o.abs()) / (1 + h) - h * size + (2.0 ** -16 + 2.0 ** -19) * size
+    _within(out, o, (1 + h) * arithmetic + h * o.abs())
+    _within(lse, l, lb)
+
+
+@pytest.mark.parametrize("Hq,new", [(4, 1), (8, 4), (16, 4)])
+def test_infinite_values_that_are_seen(Hq, new):
+    """An infinity among the seen values is the sum, both signs are NaN, other channels keep their bits;
+    keys of small weight (e^-60 of the largest) among them."""
+    seq, lens, D = [300], [new], 64
+    q, kc, vc, table, sl, _ = _attend_inputs(BF16, BF16, D, Hq, 1, 16, "heads", seq, lens)
+    slopes = torch.full((Hq,), 0.25, device="cuda")   # key 17 lies about 280 keys back: e^-70
+    opt = dict(cu_seqlens=_cu(lens), max_q=new, alibi_slopes=slopes)
+    clean, _ = _attend(q, kc, vc, table, sl, **opt)
+    inf = math.inf
+    for j, c, x in ((17, 5, inf), (250, 6, -inf), (290, 7, inf), (100, 8, -inf), (90, 9, inf), (91, 9, -inf)):
+        vc[int(table[0, j // 16]), :, j % 16, c] = x
+    out, _ = _attend(q, kc, vc, table, sl, **opt)
+    want = clean.clone()
+    want[..., 5] = want[..., 7] = inf
+    want[..., 6] = want[..., 8] = -inf
+    want[..., 9] = math.nan
+    assert torch.equal(out.isnan(), want.isnan())
+    assert torch.equal(out.nan_to_num(nan=0.0), want.nan_to_num(nan=0.0))
