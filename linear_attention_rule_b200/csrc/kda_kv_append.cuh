@@ -32,6 +32,7 @@ struct Params {
     const float* inv_freq;
     const int32_t* positions;
     int32_t rot, axis_end[4], adjacent, parts;   // parts: warps of a token
+    uint32_t blocks;                                // CTAs of the tokens
     kv::Cache c;
 };
 
@@ -74,31 +75,40 @@ template <> struct Vec8<__nv_fp8_e4m3> {
     }
 };
 
-// The sequence of token t: the last n with cu[n] <= t, found by the 32 lanes of a warp
-// together (each step keeps one of 32 parts).  -1 for padding, or where cu is inconsistent
-// around t (reported).
+// Whether the entries of sequence n are consistent; whether it has token t and they are.
+__device__ __forceinline__ bool consistent(const Params& P, int n, int a, int b) {
+    return a >= 0 && b >= a && b <= P.total && (n > 0 || a == 0);
+}
+__device__ __forceinline__ bool has_token(const Params& P, int n, int t) {
+    const int a = P.cu[n], b = P.cu[n + 1];
+    return a <= t && t < b && consistent(P, n, a, b);
+}
+// A sequence that has token t, -1 for none, by the 32 lanes of a warp together.  Entries that rise are searched: the
+// first n with cu[n + 1] > t (each step keeps one of 32 parts).  Where that is no sequence of the token's, it is padding
+// or an inconsistent entry misled the search, and all are looked at (up to 32 the search has seen them all, and
+// only one that it ends at can mislead it).
 __device__ __forceinline__ int find_sequence(const Params& P, int64_t t, int lane) {
     if (!P.cu) return (int)t;
-    int lo = 0, hi = P.num_seqs;   // cu[lo] <= t; the answer lies in [lo, hi]
+    int lo = 0, hi = P.num_seqs;   // the answer lies in [lo, hi]
     while (hi - lo > 0) {
         const int step = (hi - lo + 31) / 32;
         const int at = min(lo + (lane + 1) * step, hi);
         const unsigned m = __ballot_sync(0xffffffffu, P.cu[at] <= t);
-        // entries rise, so the lanes that vote yes come first
-        const int c = __popc(m);
+        // the lanes that vote yes before the first that does not; entries that fall have others behind it
+        const int c = __clz(__brev(~m));
         const int nlo = c == 0 ? lo : min(lo + c * step, hi);
         const int nhi = c == 32 ? hi : min(lo + (c + 1) * step, hi) - 1;
         lo = nlo;
         hi = max(nhi, nlo);
         if (c == 32) { lo = hi; }
     }
-    if (lo >= P.num_seqs) return -1;   // behind the last sequence
-    const int64_t a = P.cu[lo], b = P.cu[lo + 1];
-    if (a < 0 || t < a || t >= b || b > P.total || (lo == 0 && a != 0)) {
-        if (lane == 0) kda_set_status(KDA_ERR_BAD_SEQLENS);
-        return -1;
+    if (lo < P.num_seqs ? has_token(P, lo, (int)t) : P.num_seqs <= 32) return lo < P.num_seqs ? lo : -1;
+#pragma unroll 1
+    for (int n = lane; n - lane < P.num_seqs; n += 32) {
+        const unsigned m = __ballot_sync(0xffffffffu, n < P.num_seqs && has_token(P, n, (int)t));
+        if (m) return n - lane + __ffs(m) - 1;
     }
-    return lo;
+    return -1;
 }
 
 // x / d for the quotients that are rounded to 8 bits, r = 1 / d rounded to nearest: the product's
@@ -295,6 +305,11 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 8 : 6) append_ke
     const int64_t t = id / P.parts;
     const int part = (int)(id - t * P.parts);
     kda_grid_wait();
+    if (blockIdx.x >= P.blocks) {   // the CTAs behind the tokens' look at the entries of a sequence a thread
+        const int64_t n = (int64_t)(blockIdx.x - P.blocks) * (32 * kWarps) + threadIdx.x;
+        if (n < P.num_seqs && !consistent(P, (int)n, P.cu[n], P.cu[n + 1])) kda_set_status(KDA_ERR_BAD_SEQLENS);
+        return;
+    }
     if (t >= P.total) return;
     Tok k(P, t, lane, part);
     typename Tok::Raw a[2], b[2];
@@ -318,15 +333,16 @@ cudaError_t launch(Params& P, cudaStream_t stream) {
     // call by itself): 64 tokens take 14.3 us by one warp each, 10.2 by four, 600 tokens 16.4 and 12.3; 1,500
     // tokens take 18.4 by one, 16.4 by two, 18.4 by four; prompts of 34,953 145 by one, 158 by four.
     P.parts = P.total >= 148 * 16 ? 1 : P.total >= 148 * 8 ? 2 : 4;
-    const int64_t blocks = (P.total * P.parts + kWarps - 1) / kWarps;
+    P.blocks = (uint32_t)((P.total * P.parts + kWarps - 1) / kWarps);
+    const dim3 grid(P.blocks + (P.cu ? ((uint32_t)P.num_seqs + 32 * kWarps - 1) / (32 * kWarps) : 0));
     // Two heads further ahead where a bf16 token's heads are all one warp's: 34,953 tokens of 32 + 2 x 8 heads with
     // neighbours paired take 147 us instead of 174, over e4m3 133 instead of 140.  It spills a few registers, which
     // costs where the loop is short (1,500 tokens 7.6 us instead of 7.3) or a head takes twice the registers (fp32,
     // 4 prompts: 192 us instead of 176).
     if constexpr (sizeof(T) == 2)
         if (P.parts == 1)
-            return kda_launch_chained(append_kernel<D, T, TC, true>, dim3((unsigned)blocks), 32 * kWarps, 0, stream, P);
-    return kda_launch_chained(append_kernel<D, T, TC, false>, dim3((unsigned)blocks), 32 * kWarps, 0, stream, P);
+            return kda_launch_chained(append_kernel<D, T, TC, true>, grid, 32 * kWarps, 0, stream, P);
+    return kda_launch_chained(append_kernel<D, T, TC, false>, grid, 32 * kWarps, 0, stream, P);
 }
 
 }  // namespace append

@@ -94,3 +94,40 @@ def test_infinite_values_that_are_seen(Hq, new):
     want[..., 9] = math.nan
     assert torch.equal(out.isnan(), want.isnan())
     assert torch.equal(out.nan_to_num(nan=0.0), want.nan_to_num(nan=0.0))
+
+
+BROKEN_CU = [   # entries, tokens in all
+    ([0, 5, 3], 5), ([0, 4, 2, 2], 4), ([0, 0, 6, 4, 4], 6), ([0, 3, 7], 6), ([2, 4, 6], 6), ([-1, 3, 6], 6), ([0, 3, 2 ** 31 - 1, 6], 6),
+    ([0, 3, -7, 6], 6), ([0, 0, 1, 0], 3), ([0, 2, 2, 1], 4),
+    (list(range(0, 100, 2)) + [200, 102, 104, 106, 3], 106), ([0] * 40 + [5, 9, 7] + [7] * 40, 9),
+    (list(range(70)) + [2 ** 31 - 1] + list(range(71, 80)), 79), (list(range(2000)) + [1990] * 3, 1999),
+]
+
+
+@pytest.mark.parametrize("cu,T", BROKEN_CU)
+def test_append_reports_every_inconsistent_cu_seqlens(cu, T):
+    """An entry that falls, also the last one, is reported whether a token comes to it or not; tokens of the
+    sequences whose own entries are consistent are stored, no others are."""
+    N = len(cu) - 1
+    good = [n for n in range(N) if 0 <= cu[n] <= cu[n + 1] <= T and (n > 0 or cu[0] == 0)]
+    assert len(good) < N
+    ps = 16
+    k = 1 + torch.arange(T, dtype=torch.float32)[:, None, None].expand(T, 1, 64).contiguous().cuda()
+    kc, vc = _new_cache(N, 1, ps, 64, F32, fill=0.0)
+    # sequence n has page n, its first new token row 0
+    lens = [max(cu[n + 1] - cu[n], 0) if n in set(good) else 1 for n in range(N)]
+    q = k.repeat(1, 2, 1)
+    q_out = torch.zeros_like(q)
+    kda.kda_kv_append(k, k, kc, vc, torch.arange(N, dtype=torch.int32)[:, None].contiguous().cuda(), _ints(lens), cu_seqlens=_ints(cu), q=q,
+                      q_out=q_out)
+    assert kda.kda_get_device_status() == kda.KDA_ERR_BAD_SEQLENS
+    _ok()
+    want, had = torch.zeros(N, ps), set()
+    for n in good:
+        for i, t in enumerate(range(cu[n], cu[n + 1])):
+            assert t not in had   # no two of them share a token
+            had.add(t)
+            want[n, i] = t + 1
+    assert torch.equal(kc[:, 0, :, 0].cpu(), want) and torch.equal(vc[:, 0, :, 63].cpu(), want)
+    mine = torch.tensor([t in had for t in range(T)])
+    assert torch.equal(q_out.cpu()[mine], q.cpu()[mine]) and (q_out.cpu()[~mine] == 0).all()
