@@ -419,10 +419,10 @@ kda_status kda_kv_append(const void* k, const void* v, const void* q, int64_t k_
     kda::append::Params P = {};
     const kda_status cs = check_cache(cache, dt, num_seqs, total_tokens, cu_seqlens, &P.c);
     if (cs != KDA_OK) return cs;
-    if (Hq < 0 || (Hq > 0) != (q != nullptr) || (q && !q_out)) return KDA_ERR_INVALID_ARG;
+    if (Hq < 0) return KDA_ERR_INVALID_ARG;
     if (rope) {
         if (rope->rot_dim <= 0 || rope->rot_dim > cache->D || rope->rot_dim % 16 != 0 || rope->num_axes < 1 ||
-            rope->num_axes > 4 || (rope->num_axes > 1 && !rope->positions))
+            rope->num_axes > 4)
             return KDA_ERR_INVALID_ARG;
         int64_t pairs = 0;
         for (int a = 0; a < 4; ++a) {
@@ -437,8 +437,9 @@ kda_status kda_kv_append(const void* k, const void* v, const void* q, int64_t k_
         P.inv_freq = rope->inv_freq;
         P.positions = rope->positions;
     }
-    if (num_seqs == 0 || total_tokens == 0) return KDA_OK;
-    if (!k || !v || (rope && !rope->inv_freq)) return KDA_ERR_INVALID_ARG;
+    if (num_seqs == 0 || total_tokens == 0) return KDA_OK;   // empty arrays may have no address
+    if (!k || !v || (Hq > 0) != (q != nullptr) || (q && !q_out)) return KDA_ERR_INVALID_ARG;
+    if (rope && (!rope->inv_freq || (rope->num_axes > 1 && !rope->positions))) return KDA_ERR_INVALID_ARG;
     const void* ptrs[] = {k, v, q, q_out};
     for (const void* p : ptrs)
         if (p && !aligned16(p)) return KDA_ERR_INVALID_ARG;

@@ -131,3 +131,23 @@ def test_append_reports_every_inconsistent_cu_seqlens(cu, T):
     assert torch.equal(kc[:, 0, :, 0].cpu(), want) and torch.equal(vc[:, 0, :, 63].cpu(), want)
     mine = torch.tensor([t in had for t in range(T)])
     assert torch.equal(q_out.cpu()[mine], q.cpu()[mine]) and (q_out.cpu()[~mine] == 0).all()
+
+
+def test_steps_without_tokens():
+    """No new token, with queries and positions of several axes: nothing is done, nothing is refused."""
+    D, Hq, Hkv = 64, 4, 2
+    kc, vc = _new_cache(3, Hkv, 16, D, BF16, fill=1.0)
+    table, sl = _ints([[0], [1]]), _ints([5, 0])
+    e = lambda h: torch.empty(0, h, D, dtype=BF16, device="cuda")
+    inv = torch.ones(32, device="cuda")
+    for kw in (dict(cu_seqlens=_ints([0, 0, 0])), dict(cu_seqlens=_ints([0, 0, 0]), positions=torch.empty(3, 0, dtype=torch.int32, device="cuda"),
+                                                       axis_pairs=(16, 8, 8))):
+        q_out = kda.kda_kv_append(e(Hkv), e(Hkv), kc, vc, table, sl, q=e(Hq), inv_freq=inv, **kw)
+        assert q_out.shape == (0, Hq, D)
+    kda.kda_kv_append(e(Hkv), e(Hkv), kc, vc, table[:0], sl[:0], q=e(Hq), inv_freq=inv)   # no sequence either
+    kda.kda_kv_decode(e(Hq), kc, vc, table, sl, e(Hq), cu_seqlens=_ints([0, 0, 0]))
+    pool = torch.ones(2, Hkv, D, D, device="cuda")
+    kda.kda_decode_pool(e(Hkv), e(Hkv), e(Hkv), torch.empty(0, Hkv, D, device="cuda"), torch.empty(0, Hkv, device="cuda"), pool, _ints([0, 1]),
+                        _ints([]), e(Hkv), cu_seqlens=_ints([0, 0, 0]))
+    _ok()
+    assert (kc == 1).all() and (vc == 1).all() and (pool == 1).all()
