@@ -416,7 +416,7 @@ kda_status kda_decode_pool(const void *q, const void *k, const void *v, const fl
  *                fastest to read); the strides are multiples of 16 bytes, at least D.
  *   dt           KDA_F32 (with fp32 q, k, v), KDA_BF16 or KDA_E4M3 (with bf16 ones).  A
  *                KDA_E4M3 element x of head h stands for x * k_scale[h] (v_scale[h]).
- *   k_scale, v_scale   [Hkv] fp32, positive, KDA_E4M3 only; NULL = 1
+ *   k_scale, v_scale   [Hkv] fp32, at least 2^-126 and finite, KDA_E4M3 only; NULL = 1
  *   block_table  [num_seqs, max_pages] int32, rows table_stride apart: the pages of each
  *                sequence in order; position j is row j % page_size of page
  *                block_table[n][j / page_size].  Entries of no visible position are not read.

@@ -16,6 +16,8 @@
 // prefetch made the latter 155.
 #pragma once
 
+#include <cfloat>
+
 #include "kda_kv_cache.cuh"
 #include "kda_sm100.cuh"
 
@@ -209,7 +211,8 @@ struct Token {
     static __device__ __forceinline__ void put(TC* dst, float (&x)[8], const float* scales, int h) {
         if constexpr (F8) {
             if (scales) {
-                const float d = scales[h], r = __frcp_rn(d);
+                // finite also for a subnormal d, so that 0 stays 0
+                const float d = scales[h], r = fminf(__frcp_rn(d), FLT_MAX);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) x[j] = quotient(x[j], d, r);
             }

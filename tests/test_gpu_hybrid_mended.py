@@ -151,3 +151,28 @@ def test_steps_without_tokens():
                         _ints([]), e(Hkv), cu_seqlens=_ints([0, 0, 0]))
     _ok()
     assert (kc == 1).all() and (vc == 1).all() and (pool == 1).all()
+
+
+def test_append_divides_by_scales_of_any_size():
+    """Scales from the least normal fp32 number to near the largest: the nearest e4m3 number to the fp32 quotient,
+    held at 448.  That quotient is off from the 64-bit one by half its step, 2^-24 of it, and by a scale near
+    2^-126 its remainder is rounded to 2^-149, so by 2^-24 more: so near a tie between two e4m3 numbers either
+    may stand (17.5 / 0.7 is 25.0000004, in fp32 25, and goes to 24).  Below 2^-126, outside what a scale may
+    be, zeros stay zeros all the same."""
+    scales = [2.0 ** -126, 1.7e-38, 1.1e-30, 2.0 ** -101, 0.7, 1.0, 5e20, 2.0 ** 126, 3.3e38, 2.0 ** -130, 2.0 ** -149]
+    H, D, T, normal = len(scales), 64, 5, len(scales) - 2
+    s = torch.tensor(scales, device="cuda")
+    gen = torch.Generator().manual_seed(60)
+    x = torch.randn(T, H, D, generator=gen).mul(30).cuda().double() * s.double()[:, None]
+    x[:, :, ::9] = 0.0
+    x[:, 0, 3], x[:, 0, 4], x[:, 2, 5] = 1e30, -1e30, math.inf   # beyond 448 scales
+    k = x.to(BF16)
+    kc, vc = _new_cache(1, H, 16, D, E4M3, fill=0.0)
+    kda.kda_kv_append(k, k, kc, vc, _ints([[0]]), _ints([T]), cu_seqlens=_ints([0, T]), k_scale=s, v_scale=s)
+    _ok()
+    exact = (k.double() / s.double()[:, None]).clamp(-448, 448)[:, :normal]
+    ulp = 2.0 ** (torch.floor(torch.log2(exact.abs().clamp_min(2.0 ** -6))) - 3)   # of e4m3, subnormal below 2^-6
+    for got in (kc, vc):
+        y = got[0, :, :T].transpose(0, 1).double()
+        assert torch.isfinite(y).all() and (y[:, :, ::9] == 0).all()
+        assert ((y[:, :normal] - exact).abs() <= ulp / 2 + 2.0 ** -24 * exact.abs() + 2.0 ** -24).all()
