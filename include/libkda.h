@@ -496,7 +496,7 @@ kda_status kda_kv_append(const void *k, const void *v, const void *q, int64_t k_
  * sees may be read where they share a page with ones that it sees.  The sums' order depends
  * on the call's sizes and lengths alone: the same call gives the same bits.
  * Not supported (KDA_ERR_UNSUPPORTED): pages of one row in a KDA_E4M3 cache of 64 channels;
- * strides of 2^40 bytes and more.
+ * strides of 2^40 bytes and more; a softcap below 2^-100 or above 2^100.
  */
 kda_status kda_kv_decode(const void *q, int64_t q_stride, kda_dtype dt, const kda_kv_cache *cache,
                          const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,

@@ -477,6 +477,8 @@ kda_status kda_kv_decode(const void* q, int64_t q_stride, kda_dtype dt, const kd
     if (Hq <= 0 || Hq % cache->Hkv != 0 || max_q < 1 || window < 0 || !(softcap >= 0.f) || !(scale - scale == 0.f) ||
         !(softcap - softcap == 0.f))
         return KDA_ERR_INVALID_ARG;
+    // scale / softcap has to keep its bits: subnormal ones cost a score up to 2^-150 |q . k| softcap
+    if (softcap > 0.f && (softcap < 0x1p-100f || softcap > 0x1p100f)) return KDA_ERR_UNSUPPORTED;
     if (max_q > kMaxQ || Hq > 65535 || (int64_t)num_seqs * max_q > INT32_MAX) return KDA_ERR_UNSUPPORTED;
     if (cache->dt == KDA_E4M3 && cache->D == 64 && cache->page_size == 1) return KDA_ERR_UNSUPPORTED;   // boxes of 64 bytes
     if (num_seqs == 0 || total_tokens == 0) return KDA_OK;

@@ -176,3 +176,20 @@ def test_append_divides_by_scales_of_any_size():
         y = got[0, :, :T].transpose(0, 1).double()
         assert torch.isfinite(y).all() and (y[:, :, ::9] == 0).all()
         assert ((y[:, :normal] - exact).abs() <= ulp / 2 + 2.0 ** -24 * exact.abs() + 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("dtype,cdt", [(BF16, BF16), (BF16, E4M3), (F32, F32)])
+@pytest.mark.parametrize("cap", [2.0 ** -100, 1e-20, 1e20, 2.0 ** 100])
+def test_caps_of_the_extremes(dtype, cdt, cap):
+    """The least caps leave scores of next to nothing, also those of a query of zeros; the largest none capped."""
+    seq, lens = [70, 130], [2, 1]
+    q, kc, vc, table, sl, (ks, vs) = _attend_inputs(dtype, cdt, 64, 4, 2, 16, "heads", seq, lens)
+    q = q.contiguous()
+    q[1, 2] = 0
+    out, lse = _attend(q, kc, vc, table, sl, ks, vs, cu_seqlens=_cu(lens), max_q=2, softcap=cap)
+    o, l, ob, lb = ref.attend(q, kc, vc, table, sl, lens, 0.125, softcap=cap if cap < 1 else 0.0, k_scale=ks, v_scale=vs)
+    # A cap of 1e20 or more changes a score s by s (s / cap)^2 / 3, nothing here.  By s / cap times cap it is off by four
+    # roundings more, 2^-22 |s|, |s| < 8: 2^-19 of a score, 2^-18 of a weight and of the weights' sum, values below 8.
+    big = cap > 1
+    _within(out, o, ob + big * 2 * 2.0 ** -18 * 8)
+    _within(lse, l, lb + big * 2.0 ** -19)

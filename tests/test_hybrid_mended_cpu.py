@@ -38,3 +38,14 @@ def test_steps_with_tokens_want_their_addresses():
     assert _append(_cache(), rope) == INVALID
     for bad in (dict(q=None), dict(out=None), dict(Hq=0), dict(k=None), dict(v=None)):
         assert _append(_cache(), **bad) == INVALID
+
+
+@pytest.mark.parametrize("cap", [2.0 ** -149, 2.0 ** -127, 2.0 ** -101, 2.0 ** 101, 2.0 ** 126, 3.4e38])
+def test_decode_refuses_caps_that_it_cannot_divide_by(cap):
+    """Far out the quotient of scale and cap loses its bits or overflows (0 times infinity for a score of 0)."""
+    assert _decode(_cache(), cap=cap) == kda.KDA_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("cap", [2.0 ** -100, 2.0 ** 100])
+def test_decode_takes_caps_up_to_there(cap):
+    assert _decode(_cache(), cap=cap, N=0) == OK
