@@ -164,9 +164,11 @@ kda_kv_cache cache_of(Call& call, PyObject* ko, PyObject* vo, PyObject* to, PyOb
     const at::ScalarType ty = k.scalar_type();
     if (k.dim() != 4 || (ty != at::kFloat && ty != at::kBFloat16 && ty != at::kFloat8_e4m3fn))
         fail(PyExc_ValueError, "k_cache must be [pages, Hkv, page_size, D] in float32, bfloat16 or float8_e4m3fn");
-    if (v.sizes() != k.sizes() || v.scalar_type() != ty || v.strides() != k.strides())
+    bool alike = v.sizes() == k.sizes() && v.scalar_type() == ty;
+    for (int i = 0; alike && i < 4; ++i) alike = v.stride(i) == k.stride(i) || k.size(i) <= 1;   // one of an axis: any stride
+    if (!alike)
         fail(PyExc_ValueError, "v_cache must have the shape, type and strides of k_cache");
-    if (k.stride(3) != 1) fail(PyExc_ValueError, "the caches must be dense in their last axis");
+    if (k.stride(3) != 1 || v.stride(3) != 1) fail(PyExc_ValueError, "the caches must be dense in their last axis");
     call.add(k, "k_cache");
     call.add(v, "v_cache");
     if (!THPVariable_Check(to)) fail(PyExc_TypeError, "block_table must be a torch.Tensor");

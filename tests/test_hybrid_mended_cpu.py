@@ -49,3 +49,22 @@ def test_decode_refuses_caps_that_it_cannot_divide_by(cap):
 @pytest.mark.parametrize("cap", [2.0 ** -100, 2.0 ** 100])
 def test_decode_takes_caps_up_to_there(cap):
     assert _decode(_cache(), cap=cap, N=0) == OK
+
+
+def test_strides_of_axes_of_one_do_not_matter():
+    """One kv head, one page or pages of one row: the stride of such an axis is used by nothing, and torch
+    gives it different values by how a tensor came about.  On the CPU the call ends at the device check."""
+    D = 64
+    k = torch.zeros(6, 16, D)
+    for pages, a, b in ((6, k.unsqueeze(1), k.as_strided((6, 1, 16, D), (16 * D, 7 * D, D, 1))),
+                        (1, k[:1].unsqueeze(1), k.as_strided((1, 1, 16, D), (3, 5, D, 1))),
+                        (1, torch.zeros(1, 1, 1, D), k.as_strided((1, 1, 1, D), (9 * D, 9 * D, 9 * D, 1)))):
+        ps = a.shape[2]
+        for kc, vc in ((a, b), (b, a)):
+            assert kc.stride() != vc.stride()
+            with pytest.raises(ValueError, match="must be on"):
+                kda.kda_kv_append(k=torch.zeros(4, 1, D), v=torch.zeros(4, 1, D), k_cache=kc, v_cache=vc, block_table=torch.zeros(4, 3, dtype=torch.int32),
+                                  seq_lens=torch.zeros(4, dtype=torch.int32))
+    with pytest.raises(ValueError, match="strides"):   # those of longer axes do
+        kda.kda_kv_append(k=torch.zeros(4, 1, D), v=torch.zeros(4, 1, D), k_cache=k.unsqueeze(1), v_cache=torch.zeros(6, 32, D)[:, ::2].unsqueeze(1),
+                          block_table=torch.zeros(4, 3, dtype=torch.int32), seq_lens=torch.zeros(4, dtype=torch.int32))
