@@ -139,6 +139,8 @@ def _native():
         loader = importlib.machinery.ExtensionFileLoader("kda_native", NATIVE_PATH)
         module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("kda_native", NATIVE_PATH, loader=loader))
         loader.exec_module(module)
+        if module.built_for != "kda_native for torch " + torch.__version__:
+            raise RuntimeError("%s, and torch is %s; run __graft_entry__.build()" % (module.built_for, torch.__version__))
         module.init(*(ctypes.cast(f, ctypes.c_void_p).value
                       for f in (lib.kda_decode_pool, lib.kda_kv_append, lib.kda_kv_decode)))
         _native_module = module

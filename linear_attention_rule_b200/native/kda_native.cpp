@@ -370,4 +370,11 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "kda_native", nullptr, -1, g_meth
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit_kda_native() { return PyModule_Create(&g_module); }
+// Read from the file by the build, which makes it anew for another torch, and checked when it is loaded.
+constexpr char kBuiltFor[] = "kda_native for torch " KDA_TORCH_VERSION;
+
+PyMODINIT_FUNC PyInit_kda_native() {
+    PyObject* m = PyModule_Create(&g_module);
+    if (m && PyModule_AddStringConstant(m, "built_for", kBuiltFor) < 0) Py_CLEAR(m);
+    return m;
+}
