@@ -6,7 +6,7 @@ import torch
 
 from linear_attention_rule_b200 import kda
 from tests import hybrid_reference as ref
-from tests.test_gpu_hybrid_step import BF16, E4M3, F32, _attend_inputs, _cu, _ints, _new_cache, _ok, _table, _within
+from tests.test_gpu_hybrid_step import BF16, E4M3, F32, _Stack, _attend_inputs, _cu, _ints, _new_cache, _ok, _within
 
 pytestmark = pytest.mark.gpu
 
@@ -193,3 +193,110 @@ def test_caps_of_the_extremes(dtype, cdt, cap):
     big = cap > 1
     _within(out, o, ob + big * 2 * 2.0 ** -18 * 8)
     _within(lse, l, lb + big * 2.0 ** -19)
+
+
+# ------------------------------------------------------------------------------- what was tested too loosely
+
+U = 2.0 ** -24
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,new,opt", [(64, 4, 4, 1, {}), (128, 8, 2, 1, {}), (128, 6, 1, 3, dict(cap=5.0)), (64, 8, 1, 2, dict(bias=True)),
+                                              (128, 2, 2, 1, dict(bias=True, cap=3.0))])
+def test_fp32_attention_in_full_fp32(D, Hq, Hkv, new, opt):
+    """The fp32 kernel multiplies fp32 numbers as they are.  A score is D products and sums (D U of sum |q k|), then
+    scale, cap and bias (6 U of |s|, 2^-21 of a capped score for tanh, 2 U of bias and sum).  A weight is off by its
+    score's error and by e^x's (2^-21 by ex2, 2^-21 for a score in units of log 2 below 2^3), so by 2^-20; the product with its
+    value, the sum over the keys and the division add (keys + 4) U of sum p |v|.  Inputs in two parts of 11 bits would
+    be 2^-20 of sum |q k| off, which this does not allow."""
+    cap = opt.get("cap", 0.0)
+    seq, lens = [600, 33 + new, new, 1200], [new] * 4
+    q, kc, vc, table, sl, _ = _attend_inputs(F32, F32, D, Hq, Hkv, 16, "heads", seq, lens, seed=77)
+    q = q.contiguous()
+    slopes = 2.0 ** (-8.0 * torch.arange(1, Hq + 1, device="cuda") / Hq) if opt.get("bias") else None
+    out, lse = _attend(q, kc, vc, table, sl, cu_seqlens=_cu(lens), max_q=new, softcap=cap, alibi_slopes=slopes)
+    scale, t = D ** -0.5, 0
+    for n, length in enumerate(lens):
+        j = torch.arange(seq[n], device="cuda")
+        K, V = (c[table[n].long()[j // 16], :, j % 16].double().repeat_interleave(Hq // Hkv, 1) for c in (kc, vc))
+        for i in range(length):
+            pos = seq[n] - length + i
+            k, v, x = K[:pos + 1], V[:pos + 1], q[t].double()
+            s = scale * torch.einsum("hd,jhd->hj", x, k)
+            es = scale * torch.einsum("hd,jhd->hj", x.abs(), k.abs()) * D * U + 6 * U * s.abs()
+            if cap:
+                s = cap * torch.tanh(s / cap)
+                es += 2.0 ** -21 * s.abs()
+            if slopes is not None:
+                b = slopes.double()[:, None] * (j[:pos + 1] - pos).double()
+                s, es = s + b, es + 2 * U * (b.abs() + (s + b).abs())
+            p = torch.softmax(s, -1)
+            w = p * (es + 2.0 ** -20)                      # of each weight; a little more where a bias leaves nothing of it
+            size = torch.einsum("hj,jhd->hd", p, v.abs())
+            bound = torch.einsum("hj,jhd->hd", w, v.abs()) + (w.sum(-1)[:, None] + (pos + 5) * U) * size
+            _within(out[t], torch.einsum("hj,jhd->hd", p, v).cpu(), bound.cpu() * (1 + 2.0 ** -10))
+            l = torch.logsumexp(s, -1)
+            _within(lse[t], l.cpu(), (w.sum(-1) * (1 + 2.0 ** -10) + 4 * U * l.abs() + (pos + 1) * U).cpu())
+            t += 1
+
+
+def test_two_stacks_at_once_leave_each_other_alone():
+    """Steps of two stacks on two streams: outputs of every step, states and caches of both are those of
+    the same steps alone."""
+    N, steps = 3, 12
+    one, two = [_Stack(N), _Stack(N)], [_Stack(N, seed=51), _Stack(N, seed=51)]
+    ids = _ints(list(range(N)))
+    xs = [[s.inputs(N, 100 * i + r) for r in range(steps)] for i, s in enumerate((one[0], two[0]))]
+    lens = [_ints([r + 1] * N) for r in range(steps)]
+    fresh = _ints([-1] * N)
+    torch.cuda.synchronize()
+    alone = [[s.step(x, None, l, fresh if r == 0 else ids, ids, 1) for r, (x, l) in enumerate(zip(xx, lens))]
+             for s, xx in ((one[0], xs[0]), (two[0], xs[1]))]
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    got = [[], []]
+    for r in range(steps):
+        for i, (s, stream) in enumerate(((one[1], s1), (two[1], s2))):
+            got[i].append(s.step(xs[i][r], None, lens[r], fresh if r == 0 else ids, ids, 1, stream=stream))
+    torch.cuda.synchronize()
+    _ok()
+    for a, b in zip(alone, got):
+        for (a1, a2), (b1, b2) in zip(a, b):
+            assert torch.equal(a1, b1) and torch.equal(a2, b2)
+    for a, b in (one, two):
+        assert torch.equal(a.pool, b.pool)
+        for x, y in ((a.kc, b.kc), (a.vc, b.vc)):   # rows that nothing was stored to are NaN in both
+            assert torch.equal(x.view(torch.int16), y.view(torch.int16))
+    assert not torch.equal(one[0].pool, two[0].pool)
+
+
+@pytest.mark.parametrize("dtype,cdt", [(F32, F32), (BF16, BF16), (BF16, E4M3)])
+def test_tokens_without_a_page_have_their_queries_turned(dtype, cdt):
+    """A page outside the cache, positions behind the table and before 0: keys and values of those tokens are
+    not stored anywhere, the others' are; the queries of all are turned."""
+    H, D, ps, T = 2, 64, 16, 6
+    gen = torch.Generator().manual_seed(61)
+    q, k, v = (torch.randn(T, h, D, generator=gen).to(dtype).cuda() for h in (4, H, H))
+    inv = (10000.0 ** (-torch.arange(32, dtype=torch.float64) / 32)).float()
+    for table, length in (([[0, 3]], 20), ([[0, 2]], 34), ([[1, 2]], 4), ([[-1, 0]], 18)):
+        kc, vc = _new_cache(3, H, ps, D, cdt, fill=0.0)
+        q_out = torch.full_like(q, 9.0)
+        kda.kda_kv_append(k, v, kc, vc, _ints(table), _ints([length]), cu_seqlens=_ints([0, T]), q=q, q_out=q_out, inv_freq=inv.cuda())
+        assert kda.kda_get_device_status() == kda.KDA_ERR_BAD_PAGE
+        place = torch.arange(length - T, length)
+        y, size = ref.rotate(q, place[None], inv, [32], False)
+        _within(q_out, y, ref.rotation_bound(y, size, dtype))
+        y, size = ref.rotate(k, place[None], inv, [32], False)
+        bound = ref.rotation_bound(y, size, cdt) + (2.0 ** -10 if cdt == E4M3 else 0.0)
+        want_v = v.float().to(cdt).float()
+        left_k, left_v = kc.clone().float(), vc.clone().float()
+        stored = 0
+        for t, j in enumerate(place.tolist()):
+            page = table[0][j // ps] if 0 <= j < 2 * ps else -1
+            if not 0 <= page < 3:
+                continue
+            stored += 1
+            _within(kc[page, :, j % ps].float(), y[t], bound[t])
+            assert torch.equal(vc[page, :, j % ps].float(), want_v[t])
+            left_k[page, :, j % ps] = left_v[page, :, j % ps] = 0
+        assert 0 < stored < T and (left_k == 0).all() and (left_v == 0).all()
+    _ok()
