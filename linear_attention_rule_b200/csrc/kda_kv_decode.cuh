@@ -119,16 +119,8 @@ __device__ __forceinline__ float warp_max(float x) {
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
     return y;
 }
-// Bounded wait for an mbarrier phase (about a second); false when it ran out.
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
-    if (sm100::mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (clock64() - t0 < 2000000000ll)
-        if (sm100::mbar_try_wait(bar, parity)) return true;
-    return false;
-}
-// The same by a whole warp, whose lanes leave it together: what follows (tcgen05.ld, barriers) wants
-// them so.
+// Bounded wait of a whole warp for an mbarrier phase (about a second); false when it ran out.  The lanes leave
+// it together: what follows (tcgen05.ld, barriers) wants them so.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
     if (__all_sync(0xffffffffu, sm100::mbar_try_wait(bar, parity))) return true;
     const long long t0 = clock64();
@@ -181,10 +173,6 @@ struct Meta {
     int32_t pad;
 };
 static_assert(sizeof(Meta) == 64, "laid out in shared memory");
-// Zeros, by one warp before the others look: a tile whose wait runs out is read as something valid.
-__device__ __forceinline__ void clear_meta(Meta* m, int count, int lane) {
-    for (int i = lane; i < count * (int)(sizeof(Meta) / 16); i += 32) reinterpret_cast<uint4*>(m)[i] = make_uint4(0u, 0u, 0u, 0u);
-}
 enum : int32_t { kFirst = 1, kLast = 2, kEdge = 4, kEnd = 8 };   // first, last tile of the item here; not all keys seen by all; last tile of all
 
 // The stretch of this worker, and the walk along its tiles.  An item takes a unit of the line for each of

@@ -95,7 +95,11 @@ struct SimtKernel {
         bool bad = false;
         for (int t = 0;; ++t) {
             bad |= !wait_warp(sb + C::FULL + 8 * (t % C::STG), (t / C::STG) & 1);
-            const Meta mt = *meta(t);   // after a wait that ran out another tile's or zeros, up to the vote below
+            if (bad) {   // nothing of the tile is known: the vote below, and all stop
+                bar_any(1, true, NT);
+                break;
+            }
+            const Meta mt = *meta(t);
             const uint32_t* okm = reinterpret_cast<const uint32_t*>(sm + C::OKM + (t % C::MD) * 16);
             bool all = true;   // all keys there
 #pragma unroll
@@ -263,7 +267,6 @@ struct SimtKernel {
         if (!w.few()) w.template find<C::THREADS>(reinterpret_cast<int64_t*>(sm));
         kda_grid_launch_next();
         Fetch<C, R> f{P, lane, warp == C::CW, {}};
-        if (warp == 0) clear_meta(reinterpret_cast<Meta*>(sm + C::META), C::MD, lane);
         if (warp >= C::CW) {
             if (f.keys && lane == 0) {
                 for (int i = 0; i < C::STG; ++i) {

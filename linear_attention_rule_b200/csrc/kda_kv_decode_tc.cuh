@@ -17,9 +17,9 @@
 //
 // bf16: a weight rounded to 8 bits would be the largest error by far (0.0023 of an output's size where the rounding of the
 // output alone is 0.0017).  So it goes into the product in two bf16 parts side by side in N, 2^-16 of it, whose
-// columns are summed up at an item's end.  With the scores' arithmetic two rows at a time it takes the time that one part
-// took: 186 us for 64 sequences of 512 to 16,384 keys, 171 for 32 of 8,192 with 16 rows a kv head, 183 with 32 (one part 181),
-// 264 with 64, 107 with one row of 64 channels (106).
+// columns are summed up at an item's end.  With the scores' arithmetic two rows at a time it takes about the time that one part
+// took: 185 us for 64 sequences of 512 to 16,384 keys (186), 170 for 32 of 8,192 with 16 rows a kv head (171), 180 with 32
+// (180), 264 with 64 (262), 111 with one row of 64 channels (107).
 //
 // e4m3: tcgen05 multiplies 8-bit with 8-bit operands only, and queries or weights rounded to 8 bits
 // would lose what the scores need.  So they are split into e4m3 parts that sum up to them, side by
@@ -293,7 +293,7 @@ struct TcKernel {
 
     // ------------------------------------------------------------------ products
     __device__ __forceinline__ uint8_t* v_image(int t) const { return sm + C::RING + (t % C::STG) * C::STAGE + C::RAW; }
-    __device__ __forceinline__ bool wait_full(int t) const { return wait(sb + C::FULL + 8 * (t % C::STG), (t / C::STG) & 1); }
+    __device__ __forceinline__ bool wait_full(int t) const { return wait_warp(sb + C::FULL + 8 * (t % C::STG), (t / C::STG) & 1); }
     static __device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
         if constexpr (F8) umma_f8(d, a, b, id, accumulate);
         else sm100::umma_bf16(d, a, b, id, accumulate);
@@ -480,9 +480,14 @@ struct TcKernel {
         bool bad = false;
         for (int t = 0;; ++t) {
             bad |= !wait_warp(sb + C::MFULL + 8 * (t % C::MD), (t / C::MD) & 1);
-            // After a wait that ran out this is another tile's or zeros: addresses formed from it hold, and no
-            // barrier stands before the vote below, where the group of warps stops together.
             const Meta mt = *meta(t);
+            // After a wait that ran out nothing of the tile is known.  No barrier of the group stands before the
+            // votes below, so a warp can go to them at once, and the group stops together.
+            if (bad) {
+                bar_any(bar, true, 128);
+                bar_any(bar, true, 128);
+                break;
+            }
             const bool first = mt.flags & kFirst, edge = mt.flags & kEdge;
             const int rows = min(mt.rows - row0, RW);   // of these warps; maybe none
             if (first) {
@@ -664,14 +669,15 @@ struct TcKernel {
                         *reinterpret_cast<uint4*>(at + y * (N / 8) * (TOK * 16)) = make_uint4(pk[y][0], pk[y][1], pk[y][2], pk[y][3]);
                 }
             }
-            if (!ok && row0 == 0) {   // a value row that was not fetched, or that no token sees
+            if (row0 == 0 && !__all_sync(0xffffffffu, ok)) {   // a value row that was not fetched, or that no token sees
                 bad |= !wait_full(t);
+                if (!ok)
 #pragma unroll
-                for (int ch = 0; ch < C::ROWB / 16; ++ch) *reinterpret_cast<uint4*>(v_image(t) + C::chunk(key, ch)) = make_uint4(0u, 0u, 0u, 0u);
+                    for (int ch = 0; ch < C::ROWB / 16; ++ch) *reinterpret_cast<uint4*>(v_image(t) + C::chunk(key, ch)) = make_uint4(0u, 0u, 0u, 0u);
+                __syncwarp();
             }
             if (edge && mt.nq > 1) {
                 bad |= !wait_full(t);
-                __syncwarp();
                 bad |= !sanitize(mt, t, ok, w, lane, events, pos, neg);
             }
             tc_fence_before();
@@ -782,7 +788,6 @@ struct TcKernel {
         kda_grid_launch_next();
         Fetch<C, N> f{P, lane, warp == C::SW, {}};
         if (warp == 0) sm100::tmem_alloc(sb + C::TMEM, C::TCOLS);
-        if (warp == 1) clear_meta(reinterpret_cast<Meta*>(sm + C::META), C::MD, lane);
         if (warp == C::SW || warp == C::SW + 1) {
             if (f.keys && lane == 0) {
                 for (int i = 0; i < C::STG; ++i) {

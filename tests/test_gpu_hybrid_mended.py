@@ -300,3 +300,61 @@ def test_tokens_without_a_page_have_their_queries_turned(dtype, cdt):
             left_k[page, :, j % ps] = left_v[page, :, j % ps] = 0
         assert 0 < stored < T and (left_k == 0).all() and (left_v == 0).all()
     _ok()
+
+
+def test_a_captured_step_behind_copies_and_beside_another():
+    """A graph whose step stands behind copies and a fill (no kernels), and that forks into two stacks' steps and
+    joins: replays follow new inputs, bit for bit as the steps one after another."""
+    N = 3
+    cap, ref_ = [_Stack(N), _Stack(N, seed=51)], [_Stack(N), _Stack(N, seed=51)]
+    keys = ("q", "k", "v", "g", "beta", "aq", "ak", "av")
+    src = [{k: v for k, v in s.inputs(N, 5).items() if k in keys} for s in cap]
+    x = [{k: torch.empty_like(v) for k, v in xs.items()} for xs in src]
+    ids, fresh = _ints(list(range(N))), _ints([-1] * N)
+    slots, lens = fresh.clone(), _ints([1] * N)
+    ws = [torch.empty(kda.kda_kv_decode_workspace_size(N, 4, 1, 128), dtype=torch.uint8, device="cuda") for _ in range(2)]
+
+    def both(stacks, xs, fork):
+        outs, main = [], torch.cuda.current_stream()
+        side = torch.cuda.Stream() if fork else None
+        for i, s in enumerate(stacks):
+            for k in keys:
+                xs[i][k].copy_(src[i][k])
+        if fork:
+            side.wait_stream(main)
+        for i, s in enumerate(stacks):
+            with torch.cuda.stream(side if fork and i else main):
+                ws[i].zero_()
+                outs.append(s.step(xs[i], None, lens, slots, ids, 1, ws[i]))
+        if fork:
+            main.wait_stream(side)
+        outs.append(outs[0][1].clone())
+        return outs
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        both(cap, x, False)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = both(cap, x, True)
+    for s in cap:
+        s.pool.zero_()
+    y = [{k: torch.empty_like(v) for k, v in xs.items()} for xs in src]
+    for r in range(4):
+        for i, s in enumerate(cap):
+            for k, v in s.inputs(N, 80 + 10 * i + r).items():
+                if k in keys:
+                    src[i][k].copy_(v)
+        lens.fill_(r + 1)
+        slots.copy_(fresh if r == 0 else ids)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = both(ref_, y, False)
+        torch.cuda.synchronize()
+        for (a1, a2), (b1, b2) in zip(outs[:2], want[:2]):
+            assert torch.equal(a1, b1) and torch.equal(a2, b2)
+        assert torch.equal(outs[2], want[2])
+    _ok()
+    for a, b in zip(cap, ref_):
+        assert torch.equal(a.pool, b.pool)
