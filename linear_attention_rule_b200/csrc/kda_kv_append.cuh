@@ -11,8 +11,8 @@
 // A warp has one token, or every 2nd or 4th part of one where there are few tokens.  Its lanes hold the
 // same channels of several heads, so that a lane's sines and cosines stay in registers; the first
 // loads are on their way before the token's sequence, page and angles are known.  With a CTA per token,
-// a table of sines in shared memory and the loads behind it, 9,221 tokens of 16 + 2 x 4 heads took 48 us, now 25.9;
-// 34,953 of 32 + 2 x 8 heads took 164 us, now 139 (6.2 TB/s).  Keys and values brought to L2 ahead by a
+// a table of sines in shared memory and the loads behind it, 9,221 tokens of 16 + 2 x 4 heads took 48 us, now 26.3;
+// 34,953 of 32 + 2 x 8 heads took 164 us, now 140 (6.15 TB/s).  Keys and values brought to L2 ahead by a
 // prefetch made the latter 155.
 #pragma once
 
@@ -339,9 +339,9 @@ cudaError_t launch(Params& P, cudaStream_t stream) {
     P.blocks = (uint32_t)((P.total * P.parts + kWarps - 1) / kWarps);
     const dim3 grid(P.blocks + (P.cu ? ((uint32_t)P.num_seqs + 32 * kWarps - 1) / (32 * kWarps) : 0));
     // Two heads further ahead where a bf16 token's heads are all one warp's: 34,953 tokens of 32 + 2 x 8 heads with
-    // neighbours paired take 147 us instead of 174, over e4m3 133 instead of 140.  It spills a few registers, which
-    // costs where the loop is short (1,500 tokens 7.6 us instead of 7.3) or a head takes twice the registers (fp32,
-    // 4 prompts: 192 us instead of 176).
+    // neighbours paired take 147 us instead of 174, over e4m3 133 instead of 140.  It spills 52 to 60 bytes of
+    // stores (28 to 40 without), which costs where the loop is short (1,500 tokens 7.6 us instead of 7.3) or a head takes twice
+    // the registers (fp32, 4 prompts: 192 us instead of 176).
     if constexpr (sizeof(T) == 2)
         if (P.parts == 1)
             return kda_launch_chained(append_kernel<D, T, TC, true>, grid, 32 * kWarps, 0, stream, P);

@@ -5,9 +5,10 @@
 //   m' = max(m, s_j);  l' = l 2^{m - m'} + 2^{s_j - m'};  acc' = acc 2^{m - m'} + 2^{s_j - m'} v_j.
 // Two such triples over different keys join the same way, which is how a sequence is split.
 //
-// Bound by the cache's bytes: a key and a value row serve the G = Hq / Hkv query heads of
-// their group and the sequence's new tokens (G x tokens rows), 4 D flops per row for 2 D
-// elements.  So the work is cut by bytes alone: all (sequence, kv head, row block) items are laid
+// A key and a value row serve the G = Hq / Hkv query heads of their group and the sequence's new
+// tokens (G x tokens rows), 4 D flops per row for 2 D elements.  As long as these rows are one block (up to 64
+// rows, in fp32 8) the cache is read once, and its bytes bound the kernel up to 32 rows (fp32: one); each
+// further block reads it again.  So the work is cut by bytes alone: all (sequence, kv head, row block) items are laid
 // end to end in tiles of keys, and each of 148 CTAs (one per SM) takes one equal stretch of that
 // line, whatever the lengths.  Its tiles go through a ring of shared-memory stages.  Items that lie within one stretch are
 // finished there; the others leave a partial triple per stretch, which the join kernel adds up.
@@ -539,9 +540,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
     if (lane == 0 && P.lse) P.lse[at] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
 }
 
-// Query rows that a CTA takes at a time: the least instance that holds all of a kv head's, so that keys and
-// values are read once.  4 rows as 32 took 17.4 us instead of 15.2 over 8 short sequences, 64 rows
-// in two blocks of 32 152 us instead of 119; one row of fp32 as two (16 x 4,096 keys, 8 heads of 128) 113 us instead of 102.
+// Query rows that a CTA takes at a time: the least instance that holds all that a kv head may have by max_q, so that
+// keys and values are read once; 64 (8 in fp32) where none does, and then once for every block.  4 rows as 32 took
+// 17.4 us instead of 15.2 over 8 short sequences, 64 rows in two blocks of 32 152 us instead of 119; one row of fp32 as
+// two (16 x 4,096 keys, 8 heads of 128) 112 us instead of 89.  Above the instances (32 x 8,192 bf16 keys): 64 rows 264 us,
+// 128 rows 511; fp32 (16 x 4,096 keys): 8 rows 242 us, 16 rows 464, 64 rows 1,810.  The call's lengths are on the
+// device, so a max_q above them costs: 8 heads a group with one new token 168 us with max_q = 1, 231 with 16.
 inline int block_rows(bool f32, int rows) {
     return f32 ? (rows == 1 ? 1 : rows == 2 ? 2 : 8) : (rows <= 16 ? 16 : rows <= 32 ? 32 : 64);
 }

@@ -7,7 +7,7 @@
 // Keys are TMEM lanes, so a softmax thread owns one key: it masks, scales and exponentiates the
 // rows' scores without a shuffle, keeps its own share of every row's sum, and writes its weights
 // as one 16-byte chunk per 8 rows (P MN-major without swizzle, free of bank conflicts).  Only the
-// running maximum is shared, and the tile that raises it by more than 2^8 is rare (kSlack).
+// running maximum is shared, and the tile that raises it by more than 2^8 is rare (SLACK).
 //
 // Warps: 4 for softmax and epilogue (TMEM lanes 32 w ..) for every 8 rows (16 of 64), which share
 // nothing but keys and values; then two that fetch tiles, one that issues the products, and
@@ -29,12 +29,14 @@
 //   a weight, in fp16 (2^-11), is p1 + p2 / 16 + p3 / 256 exactly, down to 2^-25 of the row's largest.
 // The products are exact and summed in fp32: 2^-25 of the sum of magnitudes over 128 products.  The
 // other way, turning the cache's tiles into fp16 images, took eight warps 1,900 cycles an operand and
-// four times the shared-memory traffic: 151 us for 75,800 keys of 8 heads, now 80.
+// four times the shared-memory traffic: 151 us for 75,800 keys of 8 heads, now 77.
 //
 // A product with M = 128 takes 124 cycles whatever its type, its operands' order and N up to 48 (measured), 16 of
 // them a bf16 tile of 128 channels: 1,980 of the 2,780 cycles in which an SM's share of the memory brings it.  A
 // softmax warp's way through a tile takes about 1,900.  So bf16 is bound by memory (6.1 to 6.4 TB/s over long
-// sequences), e4m3 by that way, at 2,100 cycles a tile where the memory would need 1,390 (4.4 TB/s).
+// sequences), e4m3 by that way, at 2,100 cycles a tile where the memory would need 1,390 (4.4 TB/s).  64 rows take 4.1 TB/s over
+// bf16 (two tiles in flight, 16 softmax warps) and 1.9 over e4m3, whose instance has 80 registers a thread and
+// spills 92 bytes of stores and 152 to 160 of loads.
 #pragma once
 
 #include "kda_kv_decode.cuh"
@@ -54,7 +56,7 @@ struct Tc {
     static constexpr int QP = F8 ? 2 : 1, PP = F8 ? 3 : 2;                    // parts of queries and weights
     // The running maximum follows the scores only when they exceed it by SLACK (in units of log 2):
     // until then acc is not rescaled.  Weights are 2^(s - m + BASE): up to 2^8, which fp32 sums and bf16
-    // weights hold as well as 1; with e4m3 parts from 2^7 (the smallest parts then lie far below the
+    // parts hold as well as 1; with e4m3 parts from 2^7 (the smallest parts then lie far below the
     // largest weight) to 2^8.75 (e4m3 ends at 448).
     static constexpr float BASE = F8 ? 7.f : 0.f, SLACK = F8 ? 1.75f : 8.f;
     static constexpr int ROWB = D * (int)sizeof(TC);                   // a cache row
