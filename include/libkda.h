@@ -495,10 +495,10 @@ kda_status kda_kv_append(const void *k, const void *v, const void *q, int64_t k_
  * of the sums and reported as KDA_ERR_BAD_PAGE.  Scores, their statistics and the sums are
  * fp32.  Over a KDA_BF16 cache the softmax weights multiply the values to 2^-16 of each
  * (an infinite value whose weight is below 2^-110 of the row's largest may give NaN); over a
- * KDA_E4M3 cache they are rounded to fp16 (and to 2^-25 of the row's largest), a query's
- * channels are held to 2^-22 of its largest, and a query with an infinity gets NaN.  Keys outside what a token
- * sees may be read where they share a page with ones that it sees.  The sums' order depends
- * on the call's sizes and lengths alone: the same call gives the same bits.
+ * KDA_E4M3 cache to 2^-13 of each (and to 2^-25 of the row's largest), a query's channels
+ * are held to 2^-22 of its largest, and a query with an infinity gets NaN.  Keys outside
+ * what a token sees may be read where they share a page with ones that it sees.  The sums'
+ * order depends on the call's sizes and lengths alone: the same call gives the same bits.
  * The cache is read once for every 64 query rows of a kv head (its query heads times the new
  * tokens), in fp32 for every 8.
  * Not supported (KDA_ERR_UNSUPPORTED): pages of one row in a KDA_E4M3 cache of 64 channels;

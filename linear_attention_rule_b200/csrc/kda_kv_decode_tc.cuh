@@ -26,10 +26,13 @@
 // side in N, which costs nothing while the long operand bounds the product:
 //   a query row is scaled by a power of two to a largest element in [2^7, 2^8); q = q1 + q2 / 16
 //     holds bf16's 8 bits, down to 2^-22 of the row's largest;
-//   a weight, in fp16 (2^-11), is p1 + p2 / 16 + p3 / 256 exactly, down to 2^-25 of the row's largest.
+//   a weight is p1 + p2 / 16 + p3 / 256, down to 2^-25 of the row's largest, to 2^-13 of itself: of a weight in [1, 2) p1
+//     leaves 2^-4 at most, p2 2^-9 and p3 2^-14, and the first remainder, rounded to fp16 so that the others take
+//     half the instructions, is off by 2^-16.  With the weight itself in fp16 (2^-11) drafts took 77 us instead of 79,
+//     and an output was off by 0.0002 of its size beside its own rounding, now by 0.00002.
 // The products are exact and summed in fp32: 2^-25 of the sum of magnitudes over 128 products.  The
 // other way, turning the cache's tiles into fp16 images, took eight warps 1,900 cycles an operand and
-// four times the shared-memory traffic: 151 us for 75,800 keys of 8 heads, now 77.
+// four times the shared-memory traffic: 151 us for 75,800 keys of 8 heads, now 79.
 //
 // A product with M = 128 takes 124 cycles whatever its type, its operands' order and N up to 48 (measured), 16 of
 // them a bf16 tile of 128 channels: 1,980 of the 2,780 cycles in which an SM's share of the memory brings it.  A
@@ -643,11 +646,15 @@ struct TcKernel {
                     const float2 sum = add2(make_float2(l[c + i], l[c + i + 1]), make_float2(a, b));
                     l[c + i] = sum.x;
                     l[c + i + 1] = sum.y;
-                    if constexpr (F8) {   // remainders are exact: fp16 has 11 bits, each part takes 4 and the sign
+                    if constexpr (F8) {   // remainders are exact, but that the first is rounded to fp16
                         const __half2 k16 = __float2half2_rn(16.f);
-                        __half2 r = __floats2half2_rn(a, b);
+                        const uint32_t e = e4m3x2(a, b);
+                        const float2 h = __half22float2(half2_of(e));
+                        const float2 rest = fma2(h, make_float2(-16.f, -16.f), mul2(make_float2(a, b), make_float2(16.f, 16.f)));
+                        __half2 r = __floats2half2_rn(rest.x, rest.y);
+                        part[0][i / 4] |= e << (16 * (i / 2 % 2));
 #pragma unroll
-                        for (int y = 0; y < 3; ++y) {
+                        for (int y = 1; y < 3; ++y) {
                             const uint32_t e = e4m3x2(r);
                             part[y][i / 4] |= e << (16 * (i / 2 % 2));
                             if (y < 2) r = __hmul2(__hsub2(r, half2_of(e)), k16);

@@ -358,3 +358,23 @@ def test_a_captured_step_behind_copies_and_beside_another():
     _ok()
     for a, b in zip(cap, ref_):
         assert torch.equal(a.pool, b.pool)
+
+
+@pytest.mark.parametrize("Hq", [4, 32, 64])
+def test_e4m3_weights_hold_more_than_fp16(Hq):
+    """Two keys with scores +-x and values +-1: the output is the difference of two weights, tanh x, and what a
+    weight loses stands alone in it.  The larger one is 2^7 and exact; the other, in [2^6, 2^7), is off by 2^-8 from its
+    third part and by 2^-10 from the first remainder's rounding to fp16, of a sum above 2^7.5: 1.25 2^-15.5 of the output's
+    unit.  Scores are off by 64 2^-24 |x| and e^x by 2^-21, half of which reaches the difference; |tanh x| < 2^-7 is
+    rounded by 2^-8 of itself.  A weight in fp16 would be off by 2^-5 of that sum, up to 2^-12.5."""
+    N, D = 64, 64
+    kc, vc = (torch.zeros(1, 1, 16, D, device="cuda") for _ in range(2))
+    kc[0, 0, 0, 0], kc[0, 0, 1, 0] = 1.0, -1.0
+    vc[0, 0, 0], vc[0, 0, 1] = 1.0, -1.0
+    gen = torch.Generator().manual_seed(62)
+    q = torch.zeros(N, Hq, D)
+    q[:, :, 0] = (torch.rand(N, Hq, generator=gen) - 0.5) * 2.0 ** -6
+    q = q.to(BF16).cuda()
+    out, _ = _attend(q, kc.to(E4M3), vc.to(E4M3), _ints([[0]] * N), _ints([2] * N), scale=1.0)
+    want = torch.tanh(q[:, :, :1].double()).expand(N, Hq, D).cpu()
+    _within(out, want, 1.25 * 2.0 ** -15.5 + 2.0 ** -18 * want.abs() + 2.0 ** -22 + 2.0 ** -8 * want.abs())
