@@ -19,7 +19,7 @@
 // output alone is 0.0017).  So it goes into the product in two bf16 parts side by side in N, 2^-16 of it, whose
 // columns are summed up at an item's end.  With the scores' arithmetic two rows at a time it takes about the time that one part
 // took: 185 us for 64 sequences of 512 to 16,384 keys (186), 170 for 32 of 8,192 with 16 rows a kv head (171), 180 with 32
-// (180), 264 with 64 (262), 111 with one row of 64 channels (107).
+// (180), 264 to 272 with 64 (262), 112 with one row of 64 channels (107).
 //
 // e4m3: tcgen05 multiplies 8-bit with 8-bit operands only, and queries or weights rounded to 8 bits
 // would lose what the scores need.  So they are split into e4m3 parts that sum up to them, side by
@@ -37,8 +37,8 @@
 // A product with M = 128 takes 124 cycles whatever its type, its operands' order and N up to 48 (measured), 16 of
 // them a bf16 tile of 128 channels: 1,980 of the 2,780 cycles in which an SM's share of the memory brings it.  A
 // softmax warp's way through a tile takes about 1,900.  So bf16 is bound by memory (6.1 to 6.4 TB/s over long
-// sequences), e4m3 by that way, at 2,100 cycles a tile where the memory would need 1,390 (4.4 TB/s).  64 rows take 4.1 TB/s over
-// bf16 (two tiles in flight, 16 softmax warps) and 1.9 over e4m3, whose instance has 80 registers a thread and
+// sequences), e4m3 by that way, at 2,100 cycles a tile where the memory would need 1,390 (4.4 TB/s).  64 rows take 4.0 TB/s over
+// bf16 (two tiles in flight, 16 softmax warps) and 1.7 over e4m3, whose instance has 80 registers a thread and
 // spills 92 bytes of stores and 152 to 160 of loads.
 #pragma once
 
