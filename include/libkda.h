@@ -494,7 +494,7 @@ kda_status kda_kv_append(const void *k, const void *v, const void *q, int64_t k_
  * Visible positions outside the block table, or on a page outside the cache, are left out
  * of the sums and reported as KDA_ERR_BAD_PAGE.  Scores, their statistics and the sums are
  * fp32.  Over a KDA_BF16 cache the softmax weights multiply the values to 2^-16 of each
- * (an infinite value whose weight is below 2^-110 of the row's largest may give NaN); over a
+ * (an infinite value whose weight is below 2^-100 of the row's largest may give NaN); over a
  * KDA_E4M3 cache to 2^-13 of each (and to 2^-25 of the row's largest), a query's channels
  * are held to 2^-22 of its largest, and a query with an infinity gets NaN.  Keys outside
  * what a token sees may be read where they share a page with ones that it sees.  The sums'

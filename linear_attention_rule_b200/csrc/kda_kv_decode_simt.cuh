@@ -8,8 +8,8 @@
 // a warp per row and another barrier a tile took half as long again.
 //
 // 16 x 4,096 keys, 8 heads of 128, 537 MB: 89 us with one row a head (6.0 TB/s), 112 with two, 154 with four, 242
-// with eight; 16 rows, two blocks that read the cache each, 464.  One row is bound by memory, several by the latency of shared memory and of the sums with
-// 8 warps an SM (8 rows: 37% of the issue slots, 51% of the load/store pipe).  Four channels of four keys
+// with eight; 16 rows, two blocks that read the cache each, 464.  One row is bound by memory, several by the
+// latency of shared memory and of the sums with 8 warps an SM (8 rows: 37% of the issue slots, 51% of the load/store pipe).  Four channels of four keys
 // a thread, a quarter of the weights' loads, changed nothing per tile and made item ends dearer.
 #pragma once
 

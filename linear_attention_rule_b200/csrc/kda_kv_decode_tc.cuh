@@ -15,11 +15,11 @@
 // of the next tile runs during the softmax of this one and the next item starts during the epilogue
 // of the last.  Tiles land in the operand images directly: TMA's swizzle is the images'.
 //
-// bf16: a weight rounded to 8 bits would be the largest error by far (0.0023 of an output's size where the rounding of the
-// output alone is 0.0017).  So it goes into the product in two bf16 parts side by side in N, 2^-16 of it, whose
-// columns are summed up at an item's end.  With the scores' arithmetic two rows at a time it takes about the time that one part
-// took: 185 us for 64 sequences of 512 to 16,384 keys (186), 170 for 32 of 8,192 with 16 rows a kv head (171), 180 with 32
-// (180), 264 to 272 with 64 (262), 112 with one row of 64 channels (107).
+// bf16: a weight rounded to 8 bits would be the largest error by far (0.0023 of an output's size where the
+// rounding of the output alone is 0.0017).  So it goes into the product in two bf16 parts side by side in N,
+// 2^-16 of it, whose columns are summed up at an item's end.  With the scores' arithmetic two rows at a time it
+// takes about the time that one part took: 185 us for 64 sequences of 512 to 16,384 keys (186), 170 for 32 of
+// 8,192 with 16 rows a kv head (171), 180 with 32 (180), 264 to 272 with 64 (262), 112 with one row of 64 channels (107).
 //
 // e4m3: tcgen05 multiplies 8-bit with 8-bit operands only, and queries or weights rounded to 8 bits
 // would lose what the scores need.  So they are split into e4m3 parts that sum up to them, side by
@@ -37,9 +37,9 @@
 // A product with M = 128 takes 124 cycles whatever its type, its operands' order and N up to 48 (measured), 16 of
 // them a bf16 tile of 128 channels: 1,980 of the 2,780 cycles in which an SM's share of the memory brings it.  A
 // softmax warp's way through a tile takes about 1,900.  So bf16 is bound by memory (6.1 to 6.4 TB/s over long
-// sequences), e4m3 by that way, at 2,100 cycles a tile where the memory would need 1,390 (4.4 TB/s).  64 rows take 4.0 TB/s over
-// bf16 (two tiles in flight, 16 softmax warps) and 1.7 over e4m3, whose instance has 80 registers a thread and
-// spills 92 bytes of stores and 152 to 160 of loads.
+// sequences), e4m3 by that way, at 2,150 cycles a tile where the memory would need 1,390 (4.3 TB/s).  64 rows take
+// 4.0 TB/s over bf16 (two tiles in flight, 16 softmax warps) and 1.7 over e4m3, whose instance has 80 registers a
+// thread and spills 92 bytes of stores and 152 to 160 of loads.
 #pragma once
 
 #include "kda_kv_decode.cuh"
@@ -77,8 +77,9 @@ struct Tc {
     static constexpr int COLS = (2 * QP + OB * PP) * N;
     static constexpr int TCOLS = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
     // A stage is free when its tile is done; queries need one slot per stage, meta is read a little longer.
-    // Where that leaves two stages and two slots would leave three (32 bf16 rows of 128 channels: 187 us instead of 232),
-    // queries get two, and wait for the item before the last to be done.
+    // Where that leaves two stages and two slots would leave three (32 bf16 rows of 128 channels: 180 us instead of 232),
+    // queries get two, and wait for the scores of the item before the last (for its tiles to be done, items of one to
+    // four tiles took 120 us instead of 110).
     static constexpr int metas(int stg) { return stg + 2; }
     static constexpr int misc(int stg) {
         return metas(stg) * 64 + metas(stg) * 16 + stg * N * 4 + N * 8 + N * 8 + 4 * N * 4 + N * 4 + 8 * (4 * stg + metas(stg) + 13) + 16 + 4 * SW + stg * 4;
@@ -86,6 +87,7 @@ struct Tc {
     static constexpr int total(int stg, int qs) { return stg * STAGE + qs * QB + PB + misc(stg); }
     static constexpr int most(int stg) { return stg > 2 && total(stg, stg) > kMaxSmem ? most(stg - 1) : stg; }
     static constexpr bool FEWQ = most(6) == 2 && total(3, 2) <= kMaxSmem;
+    static_assert(!(FEWQ && F8), "queries are free when the scores are there");
     static constexpr int STG = FEWQ ? 3 : most(6), QS = FEWQ ? 2 : STG, MD = metas(STG);
     static constexpr int BYTES = total(STG, QS);
     static_assert(BYTES <= kMaxSmem, "shared memory of a CTA");
@@ -220,8 +222,9 @@ struct TcKernel {
             w,
             [&](int t) {
                 if (aborted() || (t >= C::STG && !wait_warp(sb + C::EMPTY + 8 * (t % C::STG), (t / C::STG - 1) & 1))) return false;
-                // queries into the slot of the item before the last: its tiles, up to t - 2 at most, are done
-                return !C::FEWQ || f.keys || w.i > 0 || w.item < C::QS || wait_warp(sb + C::EMPTY + 8 * ((t - 2) % C::STG), ((t - 2) / C::STG) & 1);
+                // Queries into the slot of the item before the last: the scores of its tiles, up to t - 2 at most, are
+                // there.  (Those of t - 4 are, by the wait above, and those of t cannot be: the phase is meant.)
+                return !C::FEWQ || f.keys || w.i > 0 || w.item < C::QS || wait_warp(sb + C::SFULL + 8 * (t & 1), ((t - 2) >> 1) & 1);
             },
             [&](int t) {
                 put(f, w, t);

@@ -378,3 +378,23 @@ def test_e4m3_weights_hold_more_than_fp16(Hq):
     out, _ = _attend(q, kc.to(E4M3), vc.to(E4M3), _ints([[0]] * N), _ints([2] * N), scale=1.0)
     want = torch.tanh(q[:, :, :1].double()).expand(N, Hq, D).cpu()
     _within(out, want, 1.25 * 2.0 ** -15.5 + 2.0 ** -18 * want.abs() + 2.0 ** -22 + 2.0 ** -8 * want.abs())
+
+
+@pytest.mark.parametrize("Hq,new", [(5, 4), (8, 4)])
+def test_queries_of_short_items_wait_for_their_slot(Hq, new):
+    """Rows of 17 to 32 by 128 channels have two slots for queries and three for tiles: items of one to four tiles,
+    in orders that put one of each length behind each, with queries of very different size side by side."""
+    gen = torch.Generator().manual_seed(63)
+    N, D = 400, 128
+    seq = (new + torch.randint(0, 4, (N,), generator=gen) * 128 + torch.randint(0, 100, (N,), generator=gen)).tolist()
+    lens = [new] * N
+    q, kc, vc, table, sl, _ = _attend_inputs(BF16, BF16, D, Hq, 1, 64, "heads", seq, lens)
+    q = (q.contiguous().unflatten(0, (N, new)) * torch.tensor([4.0, 2.0 ** -6, 1.0, 0.0], device="cuda").repeat(N // 4)[:, None, None, None]).flatten(0, 1).to(BF16)
+    cu = _cu(lens)
+    out, lse = _attend(q, kc, vc, table, sl, cu_seqlens=cu, max_q=new)
+    o, l, ob, lb = ref.attend(q, kc, vc, table, sl, lens, D ** -0.5)
+    _within(out, o, ob)
+    _within(lse, l, lb)
+    for _ in range(40):
+        again, l2 = _attend(q, kc, vc, table, sl, cu_seqlens=cu, max_q=new)
+        assert torch.equal(out, again) and torch.equal(lse, l2)
