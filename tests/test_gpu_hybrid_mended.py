@@ -398,3 +398,39 @@ def test_queries_of_short_items_wait_for_their_slot(Hq, new):
     for _ in range(40):
         again, l2 = _attend(q, kc, vc, table, sl, cu_seqlens=cu, max_q=new)
         assert torch.equal(out, again) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("cu,T", [c for c in BROKEN_CU if len(c[0]) < 100])
+def test_pool_and_attention_handle_the_consistent_sequences(cu, T):
+    """Of an inconsistent cu_seqlens the consistent sequences come out as in calls of their own, and rows of no
+    such sequence are left as they were."""
+    N, D = len(cu) - 1, 64
+    good = [n for n in range(N) if 0 <= cu[n] <= cu[n + 1] <= T and (n > 0 or cu[0] == 0)]
+    gen = torch.Generator().manual_seed(64)
+    q, k, v = (torch.randn(T, 2, D, generator=gen).mul(0.2).cuda() for _ in range(3))
+    g, beta = -torch.rand(T, 2, D, generator=gen).cuda(), torch.rand(T, 2, generator=gen).cuda()
+    pool = torch.randn(N, 2, D, D, generator=gen).cuda()
+    kc, vc = (torch.randn(N, 2, 16, D, generator=gen).cuda() for _ in range(2))
+    table = torch.arange(N, dtype=torch.int32)[:, None].contiguous().cuda()
+    lens = _ints([12] * N)
+    ids = torch.arange(N, dtype=torch.int32, device="cuda")
+    out, att = (torch.full((T, 2, D), 7.0, device="cuda") for _ in range(2))
+    kda.kda_decode_pool(q, k, v, g, beta, pool, ids, _ints([-1] * T), out, cu_seqlens=_ints(cu))
+    assert kda.kda_get_device_status() == kda.KDA_ERR_BAD_SEQLENS
+    kda.kda_kv_decode(q, kc, vc, table, lens, att, cu_seqlens=_ints(cu), max_q=16)
+    assert kda.kda_get_device_status() == kda.KDA_ERR_BAD_SEQLENS
+    want, w_att = (torch.full((T, 2, D), 7.0, device="cuda") for _ in range(2))
+    for n in good:
+        a, b = cu[n], cu[n + 1]
+        if a == b:
+            continue
+        one = [x[a:b].contiguous() for x in (q, k, v, g, beta)]
+        o = torch.empty(b - a, 2, D, device="cuda")
+        kda.kda_decode_pool(*one, pool, ids[n:n + 1], _ints([-1] * (b - a)), o, cu_seqlens=_ints([0, b - a]))
+        want[a:b] = o
+        kda.kda_kv_decode(one[0], kc, vc, table[n:n + 1], lens[n:n + 1], o, cu_seqlens=_ints([0, b - a]), max_q=16)
+        w_att[a:b] = o
+    _ok()
+    assert torch.equal(out, want)
+    assert torch.allclose(att, w_att, rtol=0, atol=2.0 ** -18)   # sums of 12 weights and values of a few units, in another order
+    assert torch.equal(att == 7.0, w_att == 7.0)
